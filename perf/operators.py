@@ -339,7 +339,7 @@ def _own(s):
         return H.hinm_fp4_dequantize(q, axis=c["axis"], out=s["out"])
     if c["kind"] in ("linear", "experts") and "w" not in keep:
         keep["w"] = H.Fp4Matrix(format=fmt, batch=c.get("E", 1), rows=c["M"], depth=c["K"], values=s["w"][0],
-                                scales=s["w"][1], tensor_scale=s["w"][2])
+                                scales=s["w"][1], tensor_scale=s["w"][2] if c["fmt"] == "nv" else None)
     if c["kind"] == "linear":
         x = keep["x"] = H.hinm_fp4_quantize(s["x"], fmt, axis=c["axis"], tensor_scale=s["scale"],
                                             out=keep.get("x"))
