@@ -412,6 +412,124 @@ hinm_status hinm_spmm_epilogue(const hinm_layout* layout, const void* X, int N, 
                                const float* bias, int activation, int out_bf16, int flags,
                                void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * b1. Microscaled 4-bit matrices  (the pages compress by pruning and name no number format:
+ * this is the library's other compression of the same layers, W or W (.) M, and of the
+ * activations that meet them).
+ * A matrix of `rows` x `depth` (depth: the dimension that a product sums over) holds e2m1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one scale for each block of its depth:
+ *   HINM_FP4_NV  blocks of 16, scale s in e4m3, one fp32 scale g for each matrix:
+ *                x' = x / g (x times fl32(1/g), rounded to fp32), s = e4m3(max |x'| / 6),
+ *                code = e2m1(x' / s), value = code s g
+ *   HINM_FP4_MX  blocks of 32, scale a power of two (e8m0):
+ *                s = 2^(floor(log2 max |x|) - 2) (at least 2^-127), code = e2m1(x / s),
+ *                value = code s
+ * All roundings are to nearest, ties to even, of the exact quotient, saturating (e2m1 at 6, e4m3
+ * at 448); the value is rounded to fp32, then to the type that it is stored in.  A block with
+ * scale 0 (NV, a maximum of at most 6 * 2^-10 g) has codes of 0.  A block with a value that is
+ * not finite, or (NV) not finite over g, has the scale NaN: everything read from it, and every
+ * output that sums over it, is NaN.
+ *
+ * Storage, as the tensor cores read it:
+ *   values   batch * rows rows of D / 2 bytes, D = the stored depth: element k of a row in byte
+ *            k / 2, the even one in the low 4 bits.  D = depth rounded up to 128 (zeros there).
+ *   scales   per matrix ceil(rows / 128) tiles of D / (64 NV, 128 MX) chunks of 512 bytes; a
+ *            chunk holds 128 rows x 4 blocks: block b of row r at 16 (r mod 32) + 4 (r / 32) + b.
+ *            Rows past the last are not written.
+ * Ragged matrices hold tokens sorted by group (expert), group e's at [offsets[e], offsets[e+1])
+ * of the token dimension, which has `rows` (HINM_RAGGED_ROWS) or `depth` (HINM_RAGGED_DEPTH)
+ * places in all; tokens before the first or behind the last group are neither read nor
+ * written.  offsets: device int32 [groups + 1], nondecreasing, inside the dimension; offsets
+ * that are not set HINM_ERR_INVALID_ARG in the device status word, and nothing outside the
+ * matrices is read or written.
+ *   ragged rows:  values as above; group e's scale tiles start at tile offsets[e] / 128 + e
+ *                 (rows / 128 + groups tiles, division rounded down)
+ *   ragged depth: D = 128 (depth / 128 + groups); group e's tokens start at stored depth
+ *                 128 (offsets[e] / 128 + e), zeros up to the next multiple of 128
+ * -------------------------------------------------------------------------------- */
+#define HINM_FP4_LAYOUT_VERSION 1
+#define HINM_FP4_NV 0
+#define HINM_FP4_MX 1
+#define HINM_RAGGED_NONE 0
+#define HINM_RAGGED_ROWS 1
+#define HINM_RAGGED_DEPTH 2
+#define HINM_DTYPE_BF16 0
+#define HINM_DTYPE_F16 1
+#define HINM_DTYPE_F32 2
+
+typedef struct {
+  int32_t layout_version;  /* must be HINM_FP4_LAYOUT_VERSION */
+  int32_t format;          /* HINM_FP4_* */
+  int32_t batch;           /* matrices (experts' weights); 1 when ragged */
+  int32_t rows, depth;     /* of each */
+  int32_t ragged, groups;  /* HINM_RAGGED_*; 1..1024 groups when ragged, else 0 */
+  const int32_t* offsets;  /* device int32 [groups + 1] when ragged, else NULL */
+  uint8_t* values;         /* device, values_bytes of hinm_fp4_size */
+  uint8_t* scales;         /* device, scales_bytes */
+  float* tensor_scale;     /* NV: device fp32 [batch], > 0 and finite, or NULL (1); MX: NULL */
+} hinm_fp4;
+
+hinm_status hinm_fp4_size(int format, int batch, int rows, int depth, int ragged, int groups,
+                          size_t* values_bytes_host, size_t* scales_bytes_host);
+
+/* The source of a matrix, in the three calls below: elements of dtype HINM_DTYPE_* in
+ * row-major order, `ld` elements from row to row and batch_stride from matrix to matrix (not
+ * read when batch is 1), aligned to their own size.
+ *   axis 1: rows x depth (blocks along the source's rows), the row pitch ld >= depth
+ *   axis 0: depth x rows (blocks down its columns: the stored matrix is the transpose),
+ *           ld >= rows
+ * So W [M][K] goes in with axis 1 for Y = W X, and with axis 0 (as W^T) for dX = W^T dY;
+ * X [K][N] with axis 0, or X^T [N][K] (token by token) with axis 1.
+ * bitmask (NULL allowed; not with ragged matrices): uint32 words over the source as hinm_mask
+ * writes them, [batch][source rows][ceil(source columns / 32)]; an element whose bit is 0
+ * counts as 0 whatever it holds, NaN included.
+ *
+ * hinm_fp4_tensor_scale writes q->tensor_scale[b] = the smallest power of two g, at least
+ * 2^-126, with max |x| <= 6 * 448 g over matrix b (of a ragged matrix: over its groups);
+ * elements that are not finite are left out.  NV only; q's values and scales are not used.
+ * hinm_fp4_quantize reads q->tensor_scale and writes q->values and q->scales.
+ * hinm_fp4_dequantize writes the values back; places outside the groups keep what they hold.
+ * rows 0 (ragged rows) or depth 0 (ragged depth) is allowed: there is nothing to do.
+ * Errors: HINM_ERR_SHAPE, HINM_ERR_INVALID_ARG, HINM_ERR_ALIGNMENT, HINM_ERR_UNSUPPORTED. */
+hinm_status hinm_fp4_tensor_scale(const void* src, int dtype, long long ld, long long batch_stride,
+                                  int axis, const uint32_t* bitmask, const hinm_fp4* q,
+                                  void* stream);
+hinm_status hinm_fp4_quantize(const void* src, int dtype, long long ld, long long batch_stride,
+                              int axis, const uint32_t* bitmask, const hinm_fp4* q, void* stream);
+hinm_status hinm_fp4_dequantize(const hinm_fp4* q, int axis, void* dst, int dtype, long long ld,
+                                long long batch_stride, void* stream);
+
+/* b2. Product of two 4-bit matrices of one format:
+ *   Y[m][n] = act(gA gB sum_k A[m][k] B[n][k] + bias[m])
+ * summed in fp32 on the tensor cores over codes and block scales, rounded once to Y's type.
+ * A: rows M (a weight's output channels), B: rows N (tokens), the same depth, neither ragged,
+ * batch 1.  Y_out: dtype HINM_DTYPE_*, [M][N] with ldy >= N elements from row to row, or
+ * (transposed) [N][M] with ldy >= M; aligned to its element.  bias: device fp32 [M] or NULL.
+ * The gradients of Y = W X are products too: dX = W^T dY and dW = dY X^T, of matrices
+ * quantised along the other axis (rounding to 4 bits has the straight-through gradient).
+ *
+ * b3. Products by expert, the tokens sorted by expert and counted on the device:
+ * hinm_fp4_grouped_matmul: for every group e of B (ragged rows, groups = A's batch)
+ *   Y[m][n] = act(gA[e] gB sum_k A_e[m][k] B[n][k] + bias[e][m]),  offsets[e] <= n < offsets[e+1]
+ * Y as above with N = B's rows; columns of no group keep what they hold.  bias: fp32 [batch][M]
+ * or NULL.  The gradient with respect to X is the same call with W_e^T and dY.
+ * hinm_fp4_grouped_weight_grad: for every group e of A and B (both ragged depth, quantised with
+ * the same offsets; B's are the ones read)
+ *   Y_e[m][n] = gA gB sum_k A[m][k] B[n][k],  offsets[e] <= k < offsets[e+1]
+ * Y_out: [groups][M][N], ldy >= N, batch_stride elements from expert to expert; an expert
+ * without tokens gets zeros.
+ * Offsets that decrease or leave the matrix: status word, and nothing is written.
+ * Errors: HINM_ERR_SHAPE, HINM_ERR_INVALID_ARG, HINM_ERR_ALIGNMENT, HINM_ERR_UNSUPPORTED. */
+hinm_status hinm_fp4_matmul(const hinm_fp4* A, const hinm_fp4* B, void* Y_out, int dtype,
+                            long long ldy, int transposed, const float* bias, int activation,
+                            void* stream);
+hinm_status hinm_fp4_grouped_matmul(const hinm_fp4* A, const hinm_fp4* B, void* Y_out, int dtype,
+                                    long long ldy, int transposed, const float* bias,
+                                    int activation, void* stream);
+hinm_status hinm_fp4_grouped_weight_grad(const hinm_fp4* A, const hinm_fp4* B, void* Y_out,
+                                         int dtype, long long ldy, long long batch_stride,
+                                         void* stream);
+
 /* Diagnostic with no counterpart in the pages: launches one small kernel whose bounded
  * wait cannot complete (it waits on an mbarrier nothing arrives at), so that after about
  * limit_ns nanoseconds it records HINM_ERR_DEVICE_TIMEOUT and returns, exercising the

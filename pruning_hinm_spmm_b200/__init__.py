@@ -28,6 +28,10 @@ HINM_ERR_WORKSPACE = 8
 HINM_LAYOUT_VERSION = 2
 HINM_SPMM_TILE_PAIRS = 1   # hinm_spmm_ex flag
 HINM_ACT_NONE, HINM_ACT_RELU, HINM_ACT_SILU, HINM_ACT_GELU = 0, 1, 2, 3
+HINM_FP4_LAYOUT_VERSION = 1
+HINM_FP4_NV, HINM_FP4_MX = 0, 1
+HINM_RAGGED_NONE, HINM_RAGGED_ROWS, HINM_RAGGED_DEPTH = 0, 1, 2
+HINM_DTYPE_BF16, HINM_DTYPE_F16, HINM_DTYPE_F32 = 0, 1, 2
 
 REGION_PRUNED, REGION_24, REGION_DENSE = 0, 1, 2
 
@@ -56,6 +60,15 @@ class hinm_layout_sizes(ctypes.Structure):
                 ("meta_bytes", _sz), ("idx_dense_bytes", _sz), ("idx_sparse_bytes", _sz),
                 ("run_dense_bytes", _sz), ("run_sparse_bytes", _sz)]
 
+
+class hinm_fp4(ctypes.Structure):
+    _fields_ = [("layout_version", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("depth", ctypes.c_int32),
+                ("ragged", ctypes.c_int32), ("groups", ctypes.c_int32), ("offsets", _vp),
+                ("values", _vp), ("scales", _vp), ("tensor_scale", _vp)]
+
+
+_i64, _fp4p = ctypes.c_longlong, ctypes.POINTER(hinm_fp4)
 
 _SIGS = {
     "hinm_status_string": (ctypes.c_char_p, [_i32]),
@@ -101,6 +114,13 @@ _SIGS = {
     "hinm_spmm_ex": (_i32, [ctypes.POINTER(hinm_layout), _vp, _i32, _vp, _i32, _vp]),
     "hinm_spmm_epilogue": (_i32, [ctypes.POINTER(hinm_layout), _vp, _i32, _vp, _vp, _i32, _i32,
                                   _i32, _vp]),
+    "hinm_fp4_size": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _szp, _szp]),
+    "hinm_fp4_tensor_scale": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _fp4p, _vp]),
+    "hinm_fp4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _fp4p, _vp]),
+    "hinm_fp4_dequantize": (_i32, [_fp4p, _i32, _vp, _i32, _i64, _i64, _vp]),
+    "hinm_fp4_matmul": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i32, _vp, _i32, _vp]),
+    "hinm_fp4_grouped_matmul": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i32, _vp, _i32, _vp]),
+    "hinm_fp4_grouped_weight_grad": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i64, _vp]),
     "hinm_device_status": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32)]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -522,6 +542,262 @@ def hinm_gyro_output_round_host(I, T: int, n0, row_order, tiles, rows, kmeans_it
                                             G, k, int(kmeans_iters), cost.ctypes.data),
            "hinm_gyro_output_round_host")
     return order, (float(cost[0]), float(cost[1]))
+
+
+# ----------------------------------------------------------------------------- b1
+def hinm_fp4_size(format: int, batch: int, rows: int, depth: int, ragged: int = HINM_RAGGED_NONE,
+                  groups: int = 0) -> Tuple[int, int]:
+    """(values bytes, scales bytes) of a 4-bit matrix."""
+    v, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(_lib.hinm_fp4_size(format, batch, rows, depth, ragged, groups, ctypes.byref(v),
+                              ctypes.byref(s)), "hinm_fp4_size")
+    return int(v.value), int(s.value)
+
+
+@dataclass
+class Fp4Matrix:
+    """Device buffers of one microscaled 4-bit matrix, or of a batch of them (caller-owned torch
+    tensors; the layout is hinm.h's).  ``tensor_scale`` (HINM_FP4_NV): fp32 [batch] or None."""
+    format: int
+    batch: int
+    rows: int
+    depth: int
+    values: object                 # uint8, hinm_fp4_size()[0] bytes
+    scales: object                 # uint8, hinm_fp4_size()[1] bytes
+    tensor_scale: object = None
+    ragged: int = HINM_RAGGED_NONE
+    offsets: object = None         # int32 [groups + 1] when ragged
+    given_scale: bool = False      # tensor_scale is the caller's: "amax" never writes into it
+
+    @property
+    def groups(self) -> int:
+        return 0 if self.ragged == HINM_RAGGED_NONE else self.offsets.numel() - 1
+
+    @classmethod
+    def allocate(cls, format: int, batch: int, rows: int, depth: int, device,
+                 ragged: int = HINM_RAGGED_NONE, offsets=None) -> "Fp4Matrix":
+        torch = _torch()
+        groups = 0 if ragged == HINM_RAGGED_NONE or offsets is None else offsets.numel() - 1
+        v, s = hinm_fp4_size(format, batch, rows, depth, ragged, groups)
+        return cls(format=format, batch=batch, rows=rows, depth=depth,
+                   values=_empty_bytes(v, device), scales=_empty_bytes(s, device),
+                   tensor_scale=(torch.ones(batch, dtype=torch.float32, device=device)
+                                 if format == HINM_FP4_NV else None),
+                   ragged=ragged, offsets=offsets)
+
+    def as_c(self) -> hinm_fp4:
+        """The C struct of the buffers as they are now; checks that they are what it says."""
+        torch = _torch()
+        v, s = hinm_fp4_size(self.format, self.batch, self.rows, self.depth, self.ragged,
+                             self.groups)
+        for t, dt, n, name in ((self.values, torch.uint8, v, "values"),
+                               (self.scales, torch.uint8, s, "scales"),
+                               (self.tensor_scale, torch.float32, self.batch, "tensor_scale"),
+                               (self.offsets, torch.int32, 0, "offsets")):
+            if t is not None:
+                _device_tensor(t, name)
+                if t.dtype != dt or not t.is_contiguous() or t.numel() < n:
+                    raise ValueError(f"Fp4Matrix.{name}: need a contiguous {dt} tensor of at "
+                                     f"least {n} elements")
+        return hinm_fp4(HINM_FP4_LAYOUT_VERSION, self.format, self.batch, self.rows, self.depth,
+                        self.ragged, self.groups, _ptr(self.offsets), _ptr(self.values),
+                        _ptr(self.scales), _ptr(self.tensor_scale))
+
+
+def _device_tensor(t, name: str) -> None:
+    """Kernels run on the current device: a tensor elsewhere is refused."""
+    torch = _torch()
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: need a tensor on the current CUDA device, got {t.device}")
+
+
+def _dtype_code(t, name: str) -> int:
+    torch = _torch()
+    codes = {torch.bfloat16: HINM_DTYPE_BF16, torch.float16: HINM_DTYPE_F16,
+             torch.float32: HINM_DTYPE_F32}
+    if t.dtype not in codes:
+        raise ValueError(f"{name}: dtype {t.dtype}: need bfloat16, float16 or float32")
+    return codes[t.dtype]
+
+
+def _matrix(t, name: str, batch: Optional[int] = None):
+    """(dtype code, batch, rows, columns, ld, batch stride) of a [rows, columns] or
+    [batch, rows, columns] tensor whose last dimension is contiguous."""
+    _device_tensor(t, name)
+    code = _dtype_code(t, name)
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name}: need 2 or 3 dimensions, got {t.dim()}")
+    b, (r, c) = (t.shape[0] if t.dim() == 3 else 1), t.shape[-2:]
+    if c > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of size 1 says nothing
+    ld = t.stride(-2) if r > 1 else max(c, 1)
+    bs = t.stride(0) if t.dim() == 3 and b > 1 else 0
+    return code, b, r, c, ld, bs
+
+
+def _fp4_check_mask(bitmask, b: int, r: int, c: int):
+    torch = _torch()
+    if bitmask is not None:
+        _device_tensor(bitmask, "bitmask")
+        if (bitmask.element_size() != 4 or not bitmask.is_contiguous()
+                or bitmask.numel() != b * r * ((c + 31) // 32)):
+            raise ValueError("bitmask: need contiguous 32-bit words [batch, rows, ceil(columns / 32)] "
+                             "of the source")
+
+
+def hinm_fp4_tensor_scale(src, q: Fp4Matrix, axis: int = 1, bitmask=None, stream=None):
+    """Writes q.tensor_scale[b]: the smallest power of two g with max |src| <= 6 * 448 g, over
+    matrix b (over q's groups when ragged).  src and axis as for hinm_fp4_quantize."""
+    code, b, r, c, ld, bs = _matrix(src, "src")
+    _fp4_check_source(q, b, r, c, axis)
+    _fp4_check_mask(bitmask, b, r, c)
+    cq = q.as_c()
+    _check(_lib.hinm_fp4_tensor_scale(_ptr(src), code, ld, bs, axis, _ptr(bitmask),
+                                      ctypes.byref(cq), _stream(stream)), "hinm_fp4_tensor_scale")
+    return q.tensor_scale
+
+
+def _fp4_check_source(q: Fp4Matrix, b: int, r: int, c: int, axis: int) -> None:
+    if axis not in (0, 1):
+        raise ValueError(f"axis={axis}: need 0 or 1")
+    rows, depth = (r, c) if axis == 1 else (c, r)
+    if (q.batch, q.rows, q.depth) != (b, rows, depth):
+        raise ValueError(f"a matrix of batch {q.batch}, {q.rows} rows, depth {q.depth} does not "
+                         f"take a source of {b} x {r} x {c} with axis {axis}")
+
+
+def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scale=None,
+                      ragged: int = HINM_RAGGED_NONE, offsets=None,
+                      out: Optional[Fp4Matrix] = None, stream=None) -> Fp4Matrix:
+    """src (bf16, fp16 or fp32, [rows, depth] with axis 1, [depth, rows] with axis 0, or a batch
+    [b, ...] of them; the last dimension contiguous) in 4 bits, blocks along the depth.
+
+    ``tensor_scale`` (HINM_FP4_NV): None (1), an fp32 tensor [batch] that is used (and kept) as it
+    is, or "amax": found on the device from src (hinm_fp4_tensor_scale).  ``bitmask``: hinm_mask's
+    words over src; elements whose bit is 0 count as 0.  ``ragged`` and ``offsets`` (int32
+    [groups + 1] on the device): tokens sorted by expert along the rows or along the depth.
+    ``out``: a matrix of the same sizes to write into."""
+    code, b, r, c, ld, bs = _matrix(src, "src")
+    _fp4_check_mask(bitmask, b, r, c)
+    if out is None:
+        rows, depth = (r, c) if axis == 1 else (c, r)
+        if ragged != HINM_RAGGED_NONE and offsets is None:
+            raise ValueError("a ragged matrix needs offsets")
+        out = Fp4Matrix.allocate(format, b, rows, depth, src.device, ragged, offsets)
+    else:
+        if out.format != format or out.ragged != ragged:
+            raise ValueError("out has another format or ragged form")
+        if ragged != HINM_RAGGED_NONE:
+            if offsets is None or offsets.numel() != out.offsets.numel():
+                raise ValueError("offsets: need as many as out was made for")
+            out.offsets = offsets
+    _fp4_check_source(out, b, r, c, axis)
+    amax = isinstance(tensor_scale, str)
+    if amax and tensor_scale != "amax":
+        raise ValueError(f"tensor_scale={tensor_scale!r}: need None, a tensor or 'amax'")
+    if format == HINM_FP4_NV:
+        if tensor_scale is None:
+            out.tensor_scale = None
+        elif not amax:
+            out.tensor_scale = tensor_scale
+        elif out.tensor_scale is None or out.given_scale:
+            out.tensor_scale = _torch().empty(b, dtype=_torch().float32, device=src.device)
+        out.given_scale = tensor_scale is not None and not amax
+    elif tensor_scale is not None:
+        raise ValueError("HINM_FP4_MX has no tensor scale")
+    cq = out.as_c()
+    s = _stream(stream)
+    if amax:
+        _check(_lib.hinm_fp4_tensor_scale(_ptr(src), code, ld, bs, axis, _ptr(bitmask),
+                                          ctypes.byref(cq), s), "hinm_fp4_tensor_scale")
+    _check(_lib.hinm_fp4_quantize(_ptr(src), code, ld, bs, axis, _ptr(bitmask), ctypes.byref(cq),
+                                  s), "hinm_fp4_quantize")
+    return out
+
+
+def hinm_fp4_dequantize(q: Fp4Matrix, axis: int = 1, out=None, dtype=None, stream=None):
+    """The values of q as bf16 (or ``dtype``, or ``out``'s), [rows, depth] (axis 1) or
+    [depth, rows] (axis 0), a batch of them when q.batch > 1."""
+    torch = _torch()
+    r, c = (q.rows, q.depth) if axis == 1 else (q.depth, q.rows)
+    if out is None:
+        shape = (r, c) if q.batch == 1 else (q.batch, r, c)
+        # a ragged matrix leaves places outside its groups as they are
+        make = torch.empty if q.ragged == HINM_RAGGED_NONE else torch.zeros
+        out = make(shape, dtype=dtype or torch.bfloat16, device=q.values.device)
+    code, ob, orow, ocol, ld, bs = _matrix(out, "out")
+    _fp4_check_source(q, ob, orow, ocol, axis)
+    cq = q.as_c()
+    _check(_lib.hinm_fp4_dequantize(ctypes.byref(cq), axis, _ptr(out), code, ld, bs,
+                                    _stream(stream)), "hinm_fp4_dequantize")
+    return out
+
+
+# ----------------------------------------------------------------------------- b2, b3
+def _fp4_out(Y_out, shape, dtype, device, zero: bool = False):
+    """Y_out, or a new tensor, with its C arguments (pointer, dtype, ldy, batch stride)."""
+    torch = _torch()
+    if Y_out is None:
+        Y_out = (torch.zeros if zero else torch.empty)(shape, dtype=dtype or torch.bfloat16,
+                                                       device=device)
+    if tuple(Y_out.shape) != tuple(shape):
+        raise ValueError(f"Y_out: shape {tuple(Y_out.shape)}, need {tuple(shape)}")
+    code, b, r, c, ld, bs = _matrix(Y_out, "Y_out")
+    return Y_out, code, ld, bs
+
+
+def _fp4_bias(bias, n: int):
+    torch = _torch()
+    if bias is not None:
+        _device_tensor(bias, "bias")
+        if bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != n:
+            raise ValueError(f"bias: need {n} contiguous float32 values")
+    return _ptr(bias)
+
+
+def hinm_fp4_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None, transposed: bool = False,
+                    bias=None, activation: int = HINM_ACT_NONE, stream=None):
+    """Y [A.rows, B.rows] (transposed: [B.rows, A.rows]) = act(A B^T + bias[row of A]) as bf16 (or
+    ``dtype``, or Y_out's).  A: the weight, B: the tokens, quantised along the same depth."""
+    shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values.device)
+    ca, cb = A.as_c(), B.as_c()
+    _check(_lib.hinm_fp4_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code, ldy,
+                                1 if transposed else 0, _fp4_bias(bias, A.rows), int(activation),
+                                _stream(stream)), "hinm_fp4_matmul")
+    return Y_out
+
+
+def hinm_fp4_grouped_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None,
+                            transposed: bool = False, bias=None,
+                            activation: int = HINM_ACT_NONE, stream=None):
+    """Products by expert: the columns of Y (transposed: the rows) that belong to group e of B
+    (ragged rows) are act(A_e B^T + bias[e]).  Columns of no group keep what Y_out holds (zeros
+    when it is made here).  bias: fp32 [experts, A.rows] or None."""
+    shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values.device, zero=True)
+    ca, cb = A.as_c(), B.as_c()
+    _check(_lib.hinm_fp4_grouped_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code, ldy,
+                                        1 if transposed else 0, _fp4_bias(bias, A.batch * A.rows),
+                                        int(activation), _stream(stream)),
+           "hinm_fp4_grouped_matmul")
+    return Y_out
+
+
+def hinm_fp4_grouped_weight_grad(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None, stream=None):
+    """Y [groups, A.rows, B.rows] (fp32, or ``dtype``, or Y_out's): for each group the product of
+    its part of A's and B's ragged depth; zeros for a group without tokens."""
+    torch = _torch()
+    shape = (B.groups, A.rows, B.rows)
+    Y_out, code, ldy, bs = _fp4_out(Y_out, shape, dtype or torch.float32, A.values.device)
+    if B.groups == 1:
+        bs = (A.rows - 1) * ldy + B.rows
+    ca, cb = A.as_c(), B.as_c()
+    _check(_lib.hinm_fp4_grouped_weight_grad(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code,
+                                             ldy, bs, _stream(stream)),
+           "hinm_fp4_grouped_weight_grad")
+    return Y_out
 
 
 def hinm_device_status(stream=None) -> int:

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "../../include/hinm.h"
+#include "fp4.cuh"
 #include "hinm_internal.h"
 
 namespace {
@@ -796,6 +797,233 @@ hinm_status hinm_spmm_epilogue(const hinm_layout* layout, const void* X, int N, 
                                     hinm::device_status_ptr(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "hinm_spmm launch");
   return ok();
+}
+
+// ------------------------------------------------------------------ b1, b2, b3
+namespace {
+
+hinm_status check_fp4_shape(int format, int batch, int rows, int depth, int ragged, int groups) {
+  if (format != HINM_FP4_NV && format != HINM_FP4_MX)
+    return fail(HINM_ERR_INVALID_ARG, "unknown 4-bit format %d", format);
+  if (ragged < HINM_RAGGED_NONE || ragged > HINM_RAGGED_DEPTH)
+    return fail(HINM_ERR_INVALID_ARG, "unknown ragged form %d", ragged);
+  const bool no_rows = ragged == HINM_RAGGED_ROWS && rows == 0;
+  const bool no_depth = ragged == HINM_RAGGED_DEPTH && depth == 0;
+  if ((rows <= 0 && !no_rows) || (depth <= 0 && !no_depth) || batch <= 0)
+    return fail(HINM_ERR_SHAPE, "batch=%d, rows=%d, depth=%d must be positive", batch, rows, depth);
+  if (batch > 65535) return fail(HINM_ERR_SHAPE, "batch=%d exceeds 65535", batch);
+  if (ragged == HINM_RAGGED_NONE ? groups != 0
+                                 : groups < 1 || groups > hinm::kFp4MaxGroups)
+    return fail(HINM_ERR_SHAPE, "groups=%d: need 1..%d for a ragged matrix, else 0", groups,
+                hinm::kFp4MaxGroups);
+  if (ragged != HINM_RAGGED_NONE && batch != 1)
+    return fail(HINM_ERR_SHAPE, "batch=%d: a ragged matrix has a batch of 1", batch);
+  if (depth > 4000000) return fail(HINM_ERR_SHAPE, "depth=%d exceeds 4000000", depth);
+  if ((long long)rows * batch > 0x7FFFFF00ll)
+    return fail(HINM_ERR_SHAPE, "batch * rows = %lld exceeds 2^31", (long long)rows * batch);
+  return HINM_OK;
+}
+
+hinm_status check_fp4(const hinm_fp4* q, const char* name) {
+  if (!q) return fail(HINM_ERR_INVALID_ARG, "%s is NULL", name);
+  if (q->layout_version != HINM_FP4_LAYOUT_VERSION)
+    return fail(HINM_ERR_INVALID_ARG, "%s: layout_version=%d, need %d", name, q->layout_version,
+                HINM_FP4_LAYOUT_VERSION);
+  hinm_status st =
+      check_fp4_shape(q->format, q->batch, q->rows, q->depth, q->ragged, q->groups);
+  if (st != HINM_OK) return st;
+  if (q->ragged != HINM_RAGGED_NONE && !q->offsets)
+    return fail(HINM_ERR_INVALID_ARG, "%s: a ragged matrix needs offsets", name);
+  if (reinterpret_cast<uintptr_t>(q->offsets) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(q->tensor_scale) % 4 != 0)
+    return fail(HINM_ERR_ALIGNMENT, "%s: offsets or tensor_scale is not 4-byte aligned", name);
+  if (q->format == HINM_FP4_MX && q->tensor_scale)
+    return fail(HINM_ERR_INVALID_ARG, "%s: HINM_FP4_MX has no tensor_scale", name);
+  return HINM_OK;
+}
+
+bool fp4_empty(const hinm_fp4* q) { return q->rows == 0 || q->depth == 0; }
+
+hinm_status check_fp4_buffers(const hinm_fp4* q, const char* name) {
+  if (!q->values || !q->scales)
+    return fail(HINM_ERR_INVALID_ARG, "%s: values or scales is NULL", name);
+  if (!aligned16(q->values) || !aligned16(q->scales))
+    return fail(HINM_ERR_ALIGNMENT, "%s: values or scales is not 16-byte aligned", name);
+  return HINM_OK;
+}
+
+hinm_status check_elements(const void* p, int dtype, const char* name) {
+  if (dtype != HINM_DTYPE_BF16 && dtype != HINM_DTYPE_F16 && dtype != HINM_DTYPE_F32)
+    return fail(HINM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (!p) return fail(HINM_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % (dtype == HINM_DTYPE_F32 ? 4 : 2) != 0)
+    return fail(HINM_ERR_ALIGNMENT, "%s is not aligned to its elements", name);
+  return HINM_OK;
+}
+
+hinm_status check_fp4_source(const void* src, int dtype, long long ld, long long batch_stride,
+                             int axis, const uint32_t* bitmask, const hinm_fp4* q,
+                             const char* name) {
+  hinm_status st = check_elements(src, dtype, name);
+  if (st != HINM_OK) return st;
+  if (axis != 0 && axis != 1) return fail(HINM_ERR_INVALID_ARG, "axis=%d: need 0 or 1", axis);
+  const int cols = axis == 1 ? q->depth : q->rows, rows = axis == 1 ? q->rows : q->depth;
+  if (ld < cols) return fail(HINM_ERR_SHAPE, "ld=%lld is less than the %d columns", ld, cols);
+  if (q->batch > 1 && batch_stride < (long long)(rows - 1) * ld + cols)
+    return fail(HINM_ERR_SHAPE, "batch_stride=%lld: the matrices overlap", batch_stride);
+  if (bitmask) {
+    if (q->ragged != HINM_RAGGED_NONE)
+      return fail(HINM_ERR_UNSUPPORTED, "a ragged matrix takes no bitmask");
+    if (reinterpret_cast<uintptr_t>(bitmask) % 4 != 0)
+      return fail(HINM_ERR_ALIGNMENT, "bitmask is not 4-byte aligned");
+  }
+  return HINM_OK;
+}
+
+hinm_status check_fp4_product(const hinm_fp4* A, const hinm_fp4* B, const void* Y, int dtype,
+                              long long ldy, int transposed, const float* bias, int act) {
+  if (A->format != B->format)
+    return fail(HINM_ERR_INVALID_ARG, "A and B have different 4-bit formats");
+  if (A->depth != B->depth)
+    return fail(HINM_ERR_SHAPE, "depths differ: A %d, B %d", A->depth, B->depth);
+  if (act < HINM_ACT_NONE || act > HINM_ACT_GELU)
+    return fail(HINM_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (reinterpret_cast<uintptr_t>(bias) % 4 != 0)
+    return fail(HINM_ERR_ALIGNMENT, "bias is not 4-byte aligned");
+  const int cols = transposed ? A->rows : B->rows;
+  if (ldy < cols) return fail(HINM_ERR_SHAPE, "ldy=%lld is less than the %d columns", ldy, cols);
+  hinm_status st = check_elements(Y, dtype, "Y_out");
+  if (st != HINM_OK) return st;
+  st = check_fp4_buffers(A, "A");
+  if (st != HINM_OK) return st;
+  return check_fp4_buffers(B, "B");
+}
+
+hinm_status fp4_product(const hinm_fp4* A, const hinm_fp4* B, const hinm::Fp4Out& o, void* stream,
+                        const char* where) {
+  int* status = hinm::device_status_ptr();
+  if (!status) return fail(HINM_ERR_CUDA, "no device status word");
+  cudaError_t e = hinm::launch_fp4_matmul(*A, *B, o, status, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  return ok();
+}
+
+}  // namespace
+
+hinm_status hinm_fp4_size(int format, int batch, int rows, int depth, int ragged, int groups,
+                          size_t* values_bytes_host, size_t* scales_bytes_host) {
+  if (!values_bytes_host || !scales_bytes_host)
+    return fail(HINM_ERR_INVALID_ARG, "values_bytes_host or scales_bytes_host is NULL");
+  hinm_status st = check_fp4_shape(format, batch, rows, depth, ragged, groups);
+  if (st != HINM_OK) return st;
+  const hinm::Fp4Geom g = hinm::fp4_geom(rows, depth, ragged, groups);
+  *values_bytes_host = (size_t)batch * (size_t)rows * (size_t)g.pitch();
+  *scales_bytes_host = (size_t)batch * (size_t)g.row_tiles * (size_t)g.chunks(format) *
+                       (size_t)hinm::kFp4ChunkBytes;
+  return ok();
+}
+
+hinm_status hinm_fp4_tensor_scale(const void* src, int dtype, long long ld, long long batch_stride,
+                                  int axis, const uint32_t* bitmask, const hinm_fp4* q,
+                                  void* stream) {
+  hinm_status st = check_fp4(q, "q");
+  if (st != HINM_OK) return st;
+  if (q->format != HINM_FP4_NV)
+    return fail(HINM_ERR_UNSUPPORTED, "only HINM_FP4_NV has a tensor scale");
+  if (!q->tensor_scale) return fail(HINM_ERR_INVALID_ARG, "q: tensor_scale is NULL");
+  if (!fp4_empty(q)) {
+    st = check_fp4_source(src, dtype, ld, batch_stride, axis, bitmask, q, "src");
+    if (st != HINM_OK) return st;
+  }
+  cudaError_t e = hinm::launch_fp4_tensor_scale(src, dtype, ld, batch_stride, axis, bitmask, *q,
+                                                static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "hinm_fp4_tensor_scale launch");
+  return ok();
+}
+
+hinm_status hinm_fp4_quantize(const void* src, int dtype, long long ld, long long batch_stride,
+                              int axis, const uint32_t* bitmask, const hinm_fp4* q, void* stream) {
+  hinm_status st = check_fp4(q, "q");
+  if (st != HINM_OK) return st;
+  if (fp4_empty(q)) return ok();
+  st = check_fp4_source(src, dtype, ld, batch_stride, axis, bitmask, q, "src");
+  if (st != HINM_OK) return st;
+  st = check_fp4_buffers(q, "q");
+  if (st != HINM_OK) return st;
+  int* status = hinm::device_status_ptr();
+  if (!status) return fail(HINM_ERR_CUDA, "no device status word");
+  cudaError_t e = hinm::launch_fp4_quantize(src, dtype, ld, batch_stride, axis, bitmask, *q,
+                                            status, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "hinm_fp4_quantize launch");
+  return ok();
+}
+
+hinm_status hinm_fp4_dequantize(const hinm_fp4* q, int axis, void* dst, int dtype, long long ld,
+                                long long batch_stride, void* stream) {
+  hinm_status st = check_fp4(q, "q");
+  if (st != HINM_OK) return st;
+  if (fp4_empty(q)) return ok();
+  st = check_fp4_source(dst, dtype, ld, batch_stride, axis, nullptr, q, "dst");
+  if (st != HINM_OK) return st;
+  st = check_fp4_buffers(q, "q");
+  if (st != HINM_OK) return st;
+  int* status = hinm::device_status_ptr();
+  if (!status) return fail(HINM_ERR_CUDA, "no device status word");
+  cudaError_t e = hinm::launch_fp4_dequantize(*q, axis, dst, dtype, ld, batch_stride, status,
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "hinm_fp4_dequantize launch");
+  return ok();
+}
+
+hinm_status hinm_fp4_matmul(const hinm_fp4* A, const hinm_fp4* B, void* Y_out, int dtype,
+                            long long ldy, int transposed, const float* bias, int activation,
+                            void* stream) {
+  hinm_status st = check_fp4(A, "A");
+  if (st == HINM_OK) st = check_fp4(B, "B");
+  if (st != HINM_OK) return st;
+  if (A->ragged != HINM_RAGGED_NONE || B->ragged != HINM_RAGGED_NONE)
+    return fail(HINM_ERR_UNSUPPORTED, "ragged matrices go to the grouped products");
+  if (A->batch != 1 || B->batch != 1)
+    return fail(HINM_ERR_SHAPE, "batches A %d, B %d: need 1", A->batch, B->batch);
+  st = check_fp4_product(A, B, Y_out, dtype, ldy, transposed, bias, activation);
+  if (st != HINM_OK) return st;
+  return fp4_product(A, B, hinm::Fp4Out{Y_out, dtype, ldy, 0, transposed ? 1 : 0, bias, activation},
+                     stream, "hinm_fp4_matmul launch");
+}
+
+hinm_status hinm_fp4_grouped_matmul(const hinm_fp4* A, const hinm_fp4* B, void* Y_out, int dtype,
+                                    long long ldy, int transposed, const float* bias,
+                                    int activation, void* stream) {
+  hinm_status st = check_fp4(A, "A");
+  if (st == HINM_OK) st = check_fp4(B, "B");
+  if (st != HINM_OK) return st;
+  if (A->ragged != HINM_RAGGED_NONE || B->ragged != HINM_RAGGED_ROWS)
+    return fail(HINM_ERR_UNSUPPORTED, "need a batch of matrices A and B with ragged rows");
+  if (A->batch != B->groups)
+    return fail(HINM_ERR_SHAPE, "A has %d matrices, B %d groups", A->batch, B->groups);
+  if (fp4_empty(B)) return ok();
+  st = check_fp4_product(A, B, Y_out, dtype, ldy, transposed, bias, activation);
+  if (st != HINM_OK) return st;
+  return fp4_product(A, B, hinm::Fp4Out{Y_out, dtype, ldy, 0, transposed ? 1 : 0, bias, activation},
+                     stream, "hinm_fp4_grouped_matmul launch");
+}
+
+hinm_status hinm_fp4_grouped_weight_grad(const hinm_fp4* A, const hinm_fp4* B, void* Y_out,
+                                         int dtype, long long ldy, long long batch_stride,
+                                         void* stream) {
+  hinm_status st = check_fp4(A, "A");
+  if (st == HINM_OK) st = check_fp4(B, "B");
+  if (st != HINM_OK) return st;
+  if (A->ragged != HINM_RAGGED_DEPTH || B->ragged != HINM_RAGGED_DEPTH)
+    return fail(HINM_ERR_UNSUPPORTED, "need A and B with ragged depth");
+  if (A->groups != B->groups)
+    return fail(HINM_ERR_SHAPE, "A has %d groups, B %d", A->groups, B->groups);
+  st = check_fp4_product(A, B, Y_out, dtype, ldy, 0, nullptr, HINM_ACT_NONE);
+  if (st != HINM_OK) return st;
+  if (batch_stride < (long long)(A->rows - 1) * ldy + B->rows)
+    return fail(HINM_ERR_SHAPE, "batch_stride=%lld: the experts' outputs overlap", batch_stride);
+  return fp4_product(A, B, hinm::Fp4Out{Y_out, dtype, ldy, batch_stride, 0, nullptr, HINM_ACT_NONE},
+                     stream, "hinm_fp4_grouped_weight_grad launch");
 }
 
 hinm_status hinm_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {

@@ -155,6 +155,28 @@ struct SpmmOut {
 cudaError_t launch_spmm(const hinm_layout& L, const uint16_t* X, int N, const SpmmOut& o,
                         bool tile_pairs, int* status, cudaStream_t s);
 
+// Microscaled 4-bit matrices (arguments checked by the caller).
+cudaError_t launch_fp4_tensor_scale(const void* src, int dtype, long long ld,
+                                    long long batch_stride, int axis, const uint32_t* bits,
+                                    const hinm_fp4& q, cudaStream_t s);
+cudaError_t launch_fp4_quantize(const void* src, int dtype, long long ld, long long batch_stride,
+                                int axis, const uint32_t* bits, const hinm_fp4& q, int* status,
+                                cudaStream_t s);
+cudaError_t launch_fp4_dequantize(const hinm_fp4& q, int axis, void* dst, int dtype, long long ld,
+                                  long long batch_stride, int* status, cudaStream_t s);
+// B's ragged form says which product: of two matrices, by expert over ragged rows (columns of
+// Y), or by expert over a ragged depth (batch_stride elements between the experts' Y).
+struct Fp4Out {
+  void* Y;
+  int dtype;
+  long long ldy, batch_stride;
+  int transposed;
+  const float* bias;
+  int act;
+};
+cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out& o, int* status,
+                              cudaStream_t s);
+
 // Shared by the rank users (search and mask): V (fp64 column sums per tile) and the rank
 // of every working position.
 // tile_pmax (int [M/T]) receives each tile's largest fp32 exponent; scratch holds

@@ -203,6 +203,31 @@ __device__ __forceinline__ void mma_sp_bf16(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// D[tmem] (+)= (A sfa) * (B sfb): e2m1 operands, 64 of depth, with the block scales of A and B
+// read from tensor memory (blocks of 16 of the depth with e4m3 scales, or of 32 with e8m0).
+__device__ __forceinline__ void mma_fp4_block16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_fp4_block32(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive on `bar` once every previously issued tcgen05 operation of this thread completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -213,6 +238,13 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 // Shared memory (128 rows x 16 bytes, described by `desc`) -> tensor memory (128 lanes x 4 cols).
 __device__ __forceinline__ void tc_cp_128x128b(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.128x128b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Shared memory (32 rows x 16 bytes) -> tensor memory (32 lanes x 4 cols, in all four lane
+// quadrants).
+__device__ __forceinline__ void tc_cp_32x128b_x4(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
 }
 
 // 32 lanes x 32 consecutive fp32 columns: thread l of the warp gets lane (taddr.lane + l).
@@ -268,6 +300,21 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int n, int b_mn_major, i
   d |= uint32_t(b_mn_major & 1) << 16; // B major
   d |= uint32_t((n >> 3) & 0x3F) << 17;
   d |= uint32_t((128 >> 4) & 0x1F) << 24;
+  return d;
+}
+
+// Instruction descriptor, block-scaled e2m1: fp32 accumulator, both operands K-major, M = 128,
+// N = n.  e8m0: the scales' type (0: e4m3).  sf: which of the four scale bytes of a
+// tensor-memory word the instruction starts at (both operands; 0 or 2).
+__host__ __device__ __forceinline__ uint32_t idesc_fp4(int n, int e8m0, int sf) {
+  uint32_t d = 0;
+  d |= uint32_t(sf & 3) << 4;          // B scales' first byte
+  d |= 1u << 7;                        // A format: e2m1
+  d |= 1u << 10;                       // B format: e2m1
+  d |= uint32_t((n >> 3) & 0x3F) << 17;
+  d |= uint32_t(e8m0 & 1) << 23;       // scale type
+  d |= 1u << 27;                       // M = 128
+  d |= uint32_t(sf & 3) << 29;         // A scales' first byte
   return d;
 }
 
