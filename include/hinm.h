@@ -462,7 +462,7 @@ typedef struct {
   int32_t format;          /* HINM_FP4_* */
   int32_t batch;           /* matrices (experts' weights); 1 when ragged */
   int32_t rows, depth;     /* of each */
-  int32_t ragged, groups;  /* HINM_RAGGED_*; 1..1024 groups when ragged, else 0 */
+  int32_t ragged, groups;  /* HINM_RAGGED_*; 1..512 groups when ragged, else 0 */
   const int32_t* offsets;  /* device int32 [groups + 1] when ragged, else NULL */
   uint8_t* values;         /* device, values_bytes of hinm_fp4_size */
   uint8_t* scales;         /* device, scales_bytes */

@@ -157,6 +157,17 @@ def _stream(stream=None) -> int:
     return int(s.cuda_stream)
 
 
+def _current(t, name: str, stream=None) -> Tuple[int, int]:
+    """(current device, raw stream handle).  Kernels run on the current device: a tensor that
+    lives elsewhere is refused.  The same stream as _stream(), without making a
+    torch.cuda.Stream object for it (3 us of the host's time in a call of 10)."""
+    C = _torch()._C
+    dev = t.get_device()
+    if dev < 0 or dev != C._cuda_getDevice():
+        raise ValueError(f"{name}: need a tensor on the current CUDA device, got {t.device}")
+    return dev, (C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream))
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
@@ -585,86 +596,105 @@ class Fp4Matrix:
                                  if format == HINM_FP4_NV else None),
                    ragged=ragged, offsets=offsets)
 
-    def as_c(self) -> hinm_fp4:
-        """The C struct of the buffers as they are now; checks that they are what it says."""
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_c", None)  # as_c() checks and builds again
+
+    def as_c(self, device: Optional[int] = None) -> hinm_fp4:
+        """The C struct of the buffers as they are now.  Checks that they are what it says; the
+        struct is used again until a field is set or a tensor's memory moves."""
+        v, s, g, o = self.values, self.scales, self.tensor_scale, self.offsets
+        if device is None:
+            device = _torch().cuda.current_device()
+        at = (device, v.data_ptr(), s.data_ptr(), _ptr(g), _ptr(o))
+        if self._c is not None and self._at == at:
+            return self._c
         torch = _torch()
-        v, s = hinm_fp4_size(self.format, self.batch, self.rows, self.depth, self.ragged,
-                             self.groups)
-        for t, dt, n, name in ((self.values, torch.uint8, v, "values"),
-                               (self.scales, torch.uint8, s, "scales"),
-                               (self.tensor_scale, torch.float32, self.batch, "tensor_scale"),
-                               (self.offsets, torch.int32, 0, "offsets")):
+        vn, sn = hinm_fp4_size(self.format, self.batch, self.rows, self.depth, self.ragged,
+                               self.groups)
+        for t, dt, n, name in ((v, torch.uint8, vn, "values"), (s, torch.uint8, sn, "scales"),
+                               (g, torch.float32, self.batch, "tensor_scale"),
+                               (o, torch.int32, 0, "offsets")):
             if t is not None:
-                _device_tensor(t, name)
+                _device_tensor(t, name, device)
                 if t.dtype != dt or not t.is_contiguous() or t.numel() < n:
                     raise ValueError(f"Fp4Matrix.{name}: need a contiguous {dt} tensor of at "
                                      f"least {n} elements")
-        return hinm_fp4(HINM_FP4_LAYOUT_VERSION, self.format, self.batch, self.rows, self.depth,
-                        self.ragged, self.groups, _ptr(self.offsets), _ptr(self.values),
-                        _ptr(self.scales), _ptr(self.tensor_scale))
+        c = hinm_fp4(HINM_FP4_LAYOUT_VERSION, self.format, self.batch, self.rows, self.depth,
+                     self.ragged, self.groups, at[4], at[1], at[2], at[3])
+        object.__setattr__(self, "_at", at)
+        object.__setattr__(self, "_c", c)
+        return c
 
 
-def _device_tensor(t, name: str) -> None:
+def _device_tensor(t, name: str, device: int) -> None:
     """Kernels run on the current device: a tensor elsewhere is refused."""
-    torch = _torch()
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name}: need a tensor on the current CUDA device, got {t.device}")
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t, name: str) -> int:
-    torch = _torch()
-    codes = {torch.bfloat16: HINM_DTYPE_BF16, torch.float16: HINM_DTYPE_F16,
-             torch.float32: HINM_DTYPE_F32}
-    if t.dtype not in codes:
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: HINM_DTYPE_BF16, torch.float16: HINM_DTYPE_F16,
+                             torch.float32: HINM_DTYPE_F32})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name}: dtype {t.dtype}: need bfloat16, float16 or float32")
-    return codes[t.dtype]
+    return code
 
 
-def _matrix(t, name: str, batch: Optional[int] = None):
+def _matrix(t, name: str):
     """(dtype code, batch, rows, columns, ld, batch stride) of a [rows, columns] or
     [batch, rows, columns] tensor whose last dimension is contiguous."""
-    _device_tensor(t, name)
-    code = _dtype_code(t, name)
-    if t.dim() not in (2, 3):
-        raise ValueError(f"{name}: need 2 or 3 dimensions, got {t.dim()}")
-    b, (r, c) = (t.shape[0] if t.dim() == 3 else 1), t.shape[-2:]
-    if c > 1 and t.stride(-1) != 1:
+    code = _dtype_codes.get(t.dtype) if _dtype_codes else None
+    if code is None:
+        code = _dtype_code(t, name)
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        (r, c), b, bs = shape, 1, 0
+    elif len(shape) == 3:
+        b, r, c = shape
+        bs = st[0] if b > 1 else 0
+    else:
+        raise ValueError(f"{name}: need 2 or 3 dimensions, got {len(shape)}")
+    if c > 1 and st[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # the stride of a dimension of size 1 says nothing
-    ld = t.stride(-2) if r > 1 else max(c, 1)
-    bs = t.stride(0) if t.dim() == 3 and b > 1 else 0
-    return code, b, r, c, ld, bs
+    return code, b, r, c, (st[-2] if r > 1 else max(c, 1)), bs
 
 
-def _fp4_check_mask(bitmask, b: int, r: int, c: int):
-    torch = _torch()
+def _fp4_check_mask(bitmask, b: int, r: int, c: int, device: int):
     if bitmask is not None:
-        _device_tensor(bitmask, "bitmask")
+        _device_tensor(bitmask, "bitmask", device)
         if (bitmask.element_size() != 4 or not bitmask.is_contiguous()
                 or bitmask.numel() != b * r * ((c + 31) // 32)):
             raise ValueError("bitmask: need contiguous 32-bit words [batch, rows, ceil(columns / 32)] "
                              "of the source")
 
 
-def hinm_fp4_tensor_scale(src, q: Fp4Matrix, axis: int = 1, bitmask=None, stream=None):
-    """Writes q.tensor_scale[b]: the smallest power of two g with max |src| <= 6 * 448 g, over
-    matrix b (over q's groups when ragged).  src and axis as for hinm_fp4_quantize."""
-    code, b, r, c, ld, bs = _matrix(src, "src")
-    _fp4_check_source(q, b, r, c, axis)
-    _fp4_check_mask(bitmask, b, r, c)
-    cq = q.as_c()
-    _check(_lib.hinm_fp4_tensor_scale(_ptr(src), code, ld, bs, axis, _ptr(bitmask),
-                                      ctypes.byref(cq), _stream(stream)), "hinm_fp4_tensor_scale")
-    return q.tensor_scale
-
-
 def _fp4_check_source(q: Fp4Matrix, b: int, r: int, c: int, axis: int) -> None:
     if axis not in (0, 1):
         raise ValueError(f"axis={axis}: need 0 or 1")
     rows, depth = (r, c) if axis == 1 else (c, r)
-    if (q.batch, q.rows, q.depth) != (b, rows, depth):
+    if q.batch != b or q.rows != rows or q.depth != depth:
         raise ValueError(f"a matrix of batch {q.batch}, {q.rows} rows, depth {q.depth} does not "
                          f"take a source of {b} x {r} x {c} with axis {axis}")
+
+
+def hinm_fp4_tensor_scale(src, q: Fp4Matrix, axis: int = 1, bitmask=None, stream=None):
+    """Writes q.tensor_scale[b]: the smallest power of two g with max |src| <= 6 * 448 g, over
+    matrix b (over q's groups when ragged).  src and axis as for hinm_fp4_quantize."""
+    dev, s = _current(src, "src", stream)
+    code, b, r, c, ld, bs = _matrix(src, "src")
+    _fp4_check_source(q, b, r, c, axis)
+    _fp4_check_mask(bitmask, b, r, c, dev)
+    _check(_lib.hinm_fp4_tensor_scale(src.data_ptr(), code, ld, bs, axis, _ptr(bitmask),
+                                      ctypes.byref(q.as_c(dev)), s), "hinm_fp4_tensor_scale")
+    return q.tensor_scale
 
 
 def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scale=None,
@@ -678,8 +708,9 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
     words over src; elements whose bit is 0 count as 0.  ``ragged`` and ``offsets`` (int32
     [groups + 1] on the device): tokens sorted by expert along the rows or along the depth.
     ``out``: a matrix of the same sizes to write into."""
+    dev, s = _current(src, "src", stream)
     code, b, r, c, ld, bs = _matrix(src, "src")
-    _fp4_check_mask(bitmask, b, r, c)
+    _fp4_check_mask(bitmask, b, r, c, dev)
     if out is None:
         rows, depth = (r, c) if axis == 1 else (c, r)
         if ragged != HINM_RAGGED_NONE and offsets is None:
@@ -691,81 +722,81 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
         if ragged != HINM_RAGGED_NONE:
             if offsets is None or offsets.numel() != out.offsets.numel():
                 raise ValueError("offsets: need as many as out was made for")
-            out.offsets = offsets
+            if out.offsets is not offsets:
+                out.offsets = offsets
     _fp4_check_source(out, b, r, c, axis)
     amax = isinstance(tensor_scale, str)
     if amax and tensor_scale != "amax":
         raise ValueError(f"tensor_scale={tensor_scale!r}: need None, a tensor or 'amax'")
     if format == HINM_FP4_NV:
-        if tensor_scale is None:
-            out.tensor_scale = None
-        elif not amax:
-            out.tensor_scale = tensor_scale
+        if not amax:
+            if out.tensor_scale is not tensor_scale:
+                out.tensor_scale = tensor_scale
         elif out.tensor_scale is None or out.given_scale:
             out.tensor_scale = _torch().empty(b, dtype=_torch().float32, device=src.device)
-        out.given_scale = tensor_scale is not None and not amax
+        if out.given_scale == amax:
+            out.given_scale = not amax
     elif tensor_scale is not None:
         raise ValueError("HINM_FP4_MX has no tensor scale")
-    cq = out.as_c()
-    s = _stream(stream)
+    cq, p, m = ctypes.byref(out.as_c(dev)), src.data_ptr(), _ptr(bitmask)
     if amax:
-        _check(_lib.hinm_fp4_tensor_scale(_ptr(src), code, ld, bs, axis, _ptr(bitmask),
-                                          ctypes.byref(cq), s), "hinm_fp4_tensor_scale")
-    _check(_lib.hinm_fp4_quantize(_ptr(src), code, ld, bs, axis, _ptr(bitmask), ctypes.byref(cq),
-                                  s), "hinm_fp4_quantize")
+        _check(_lib.hinm_fp4_tensor_scale(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_tensor_scale")
+    _check(_lib.hinm_fp4_quantize(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_quantize")
     return out
 
 
 def hinm_fp4_dequantize(q: Fp4Matrix, axis: int = 1, out=None, dtype=None, stream=None):
     """The values of q as bf16 (or ``dtype``, or ``out``'s), [rows, depth] (axis 1) or
     [depth, rows] (axis 0), a batch of them when q.batch > 1."""
-    torch = _torch()
-    r, c = (q.rows, q.depth) if axis == 1 else (q.depth, q.rows)
+    dev, s = _current(q.values, "q", stream)
     if out is None:
+        torch = _torch()
+        r, c = (q.rows, q.depth) if axis == 1 else (q.depth, q.rows)
         shape = (r, c) if q.batch == 1 else (q.batch, r, c)
         # a ragged matrix leaves places outside its groups as they are
         make = torch.empty if q.ragged == HINM_RAGGED_NONE else torch.zeros
         out = make(shape, dtype=dtype or torch.bfloat16, device=q.values.device)
+    _device_tensor(out, "out", dev)
     code, ob, orow, ocol, ld, bs = _matrix(out, "out")
     _fp4_check_source(q, ob, orow, ocol, axis)
-    cq = q.as_c()
-    _check(_lib.hinm_fp4_dequantize(ctypes.byref(cq), axis, _ptr(out), code, ld, bs,
-                                    _stream(stream)), "hinm_fp4_dequantize")
+    _check(_lib.hinm_fp4_dequantize(ctypes.byref(q.as_c(dev)), axis, out.data_ptr(), code, ld, bs,
+                                    s), "hinm_fp4_dequantize")
     return out
 
 
 # ----------------------------------------------------------------------------- b2, b3
-def _fp4_out(Y_out, shape, dtype, device, zero: bool = False):
+def _fp4_out(Y_out, shape, dtype, like, device: int, zero: bool = False):
     """Y_out, or a new tensor, with its C arguments (pointer, dtype, ldy, batch stride)."""
-    torch = _torch()
     if Y_out is None:
+        torch = _torch()
         Y_out = (torch.zeros if zero else torch.empty)(shape, dtype=dtype or torch.bfloat16,
-                                                       device=device)
-    if tuple(Y_out.shape) != tuple(shape):
+                                                       device=like.device)
+    if Y_out.shape != shape:
         raise ValueError(f"Y_out: shape {tuple(Y_out.shape)}, need {tuple(shape)}")
+    _device_tensor(Y_out, "Y_out", device)
     code, b, r, c, ld, bs = _matrix(Y_out, "Y_out")
     return Y_out, code, ld, bs
 
 
-def _fp4_bias(bias, n: int):
-    torch = _torch()
-    if bias is not None:
-        _device_tensor(bias, "bias")
-        if bias.dtype != torch.float32 or not bias.is_contiguous() or bias.numel() != n:
-            raise ValueError(f"bias: need {n} contiguous float32 values")
-    return _ptr(bias)
+def _fp4_bias(bias, n: int, device: int):
+    if bias is None:
+        return None
+    _device_tensor(bias, "bias", device)
+    if bias.dtype != _torch().float32 or not bias.is_contiguous() or bias.numel() != n:
+        raise ValueError(f"bias: need {n} contiguous float32 values")
+    return bias.data_ptr()
 
 
 def hinm_fp4_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None, transposed: bool = False,
                     bias=None, activation: int = HINM_ACT_NONE, stream=None):
     """Y [A.rows, B.rows] (transposed: [B.rows, A.rows]) = act(A B^T + bias[row of A]) as bf16 (or
     ``dtype``, or Y_out's).  A: the weight, B: the tokens, quantised along the same depth."""
+    dev, s = _current(A.values, "A", stream)
     shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
-    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values.device)
-    ca, cb = A.as_c(), B.as_c()
-    _check(_lib.hinm_fp4_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code, ldy,
-                                1 if transposed else 0, _fp4_bias(bias, A.rows), int(activation),
-                                _stream(stream)), "hinm_fp4_matmul")
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev)
+    _check(_lib.hinm_fp4_matmul(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
+                                Y_out.data_ptr(), code, ldy, 1 if transposed else 0,
+                                _fp4_bias(bias, A.rows, dev), activation, s), "hinm_fp4_matmul")
     return Y_out
 
 
@@ -775,12 +806,12 @@ def hinm_fp4_grouped_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None,
     """Products by expert: the columns of Y (transposed: the rows) that belong to group e of B
     (ragged rows) are act(A_e B^T + bias[e]).  Columns of no group keep what Y_out holds (zeros
     when it is made here).  bias: fp32 [experts, A.rows] or None."""
+    dev, s = _current(A.values, "A", stream)
     shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
-    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values.device, zero=True)
-    ca, cb = A.as_c(), B.as_c()
-    _check(_lib.hinm_fp4_grouped_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code, ldy,
-                                        1 if transposed else 0, _fp4_bias(bias, A.batch * A.rows),
-                                        int(activation), _stream(stream)),
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev, zero=True)
+    _check(_lib.hinm_fp4_grouped_matmul(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
+                                        Y_out.data_ptr(), code, ldy, 1 if transposed else 0,
+                                        _fp4_bias(bias, A.batch * A.rows, dev), activation, s),
            "hinm_fp4_grouped_matmul")
     return Y_out
 
@@ -788,14 +819,13 @@ def hinm_fp4_grouped_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None,
 def hinm_fp4_grouped_weight_grad(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None, stream=None):
     """Y [groups, A.rows, B.rows] (fp32, or ``dtype``, or Y_out's): for each group the product of
     its part of A's and B's ragged depth; zeros for a group without tokens."""
-    torch = _torch()
+    dev, s = _current(A.values, "A", stream)
     shape = (B.groups, A.rows, B.rows)
-    Y_out, code, ldy, bs = _fp4_out(Y_out, shape, dtype or torch.float32, A.values.device)
+    Y_out, code, ldy, bs = _fp4_out(Y_out, shape, dtype or _torch().float32, A.values, dev)
     if B.groups == 1:
         bs = (A.rows - 1) * ldy + B.rows
-    ca, cb = A.as_c(), B.as_c()
-    _check(_lib.hinm_fp4_grouped_weight_grad(ctypes.byref(ca), ctypes.byref(cb), _ptr(Y_out), code,
-                                             ldy, bs, _stream(stream)),
+    _check(_lib.hinm_fp4_grouped_weight_grad(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
+                                             Y_out.data_ptr(), code, ldy, bs, s),
            "hinm_fp4_grouped_weight_grad")
     return Y_out
 

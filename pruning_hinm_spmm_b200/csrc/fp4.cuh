@@ -12,7 +12,7 @@ namespace hinm {
 constexpr int kFp4RowTile = 128;     // rows whose scales one 512-byte chunk holds
 constexpr int kFp4ChunkBytes = 512;  // 128 rows x 4 blocks
 constexpr int kFp4DepthPad = 128;    // depth is stored in multiples of it
-constexpr int kFp4MaxGroups = 1024;  // ragged groups (the products keep a table of them)
+constexpr int kFp4MaxGroups = 512;  // ragged groups (the products keep a table of them)
 
 __host__ __device__ constexpr int fp4_block(int format) { return format == HINM_FP4_NV ? 16 : 32; }
 

@@ -8,14 +8,26 @@
 // operands are stored row by row with the depth contiguous, as the instruction takes them
 // (K-major), and the scales in the 512-byte chunks that tcgen05.cp spreads over the lanes.
 //
-// A persistent CTA walks tiles of 128 rows of A by BN rows of B.  Warps:
-//   0      copies: per stage of 256 of the depth, TMA boxes of A and B (128-byte rows, 128-byte
+// The product is symmetric in its operands, so the kernel speaks of P, whose rows are the
+// accumulator's 128 lanes, and Q, whose rows are its columns.  A lane's columns are contiguous
+// in Y as [P][Q] and go out of registers in 32-byte stores.  Y [M][N] takes P = A; the
+// transposed Y [N][M] takes P = B (the tokens) once there are tokens enough to fill lanes, and
+// P = A with Y written as [Q][P] (a warp's lanes along M) for a few.
+//
+// A persistent CTA walks tiles of 128 rows of P by BN rows of Q.  Warps:
+//   0      copies: per stage of 256 of the depth, TMA boxes of P and Q (128-byte rows, 128-byte
 //          swizzle) and the chunks of their scales
 //   1      MMA: scales to tensor memory, then up to four products a stage
-//   2..5   epilogue: 32 lanes of the accumulator each
-// A stage's scales have tensor-memory columns of their own, which are written again only after
-// the stage's products are done (the same commit that frees its shared memory).  Every wait is
-// bounded (ptx.cuh); after one runs out the CTA stops, drains what it issued and returns.
+//   2..9   epilogue: 32 lanes of the accumulator and half of its columns each, 16 columns at a
+//          time in a loop that stays small (unrolled over a warp's columns it was bound by
+//          instruction fetches: one 256 x 256 tile with SiLU took 17.9 us), through a tile in
+//          shared memory, so that Y is written in whole 128-byte lines
+// The scales of a stage wait in a slot of tensor-memory columns, which is written again only
+// after the products that read it are done (the commit that frees their stage).  With few
+// tiles a cluster shares one tile's depth (SPLIT): each CTA leaves its partial sums in its own
+// shared memory, and each adds a share of the columns over all of them in rank order, so that
+// the result does not depend on timing.  Every wait is bounded (ptx.cuh); after one runs out
+// the CTA stops, drains what it issued and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +36,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "hinm_internal.h"
@@ -34,126 +47,409 @@ namespace hinm {
 namespace {
 
 constexpr int kStageDepth = 256;  // of the depth in one stage: 128-byte rows
+constexpr int kBoxRows = 64;      // rows of one TMA box
+
+// One side of the product.
+struct Side {
+  const uint8_t* scales;
+  long long tiles, chunks;  // scale tiles of one matrix; chunks of a tile
+  int rows;                 // of one matrix
+  int batched;              // one matrix for each expert
+  int ragged;               // its rows are the ragged tokens
+};
 
 struct MmArgs {
-  const uint8_t* sa;  // scales of A and B
-  const uint8_t* sb;
-  const float* ga;  // tensor scales (A: one a matrix), or null
+  Side p, q;
+  const float* ga;  // tensor scales: of A (a_batched: one for each expert) and B, or null
   const float* gb;
-  const float* bias;
+  const float* bias;  // per row of A, for each expert
   const int32_t* offsets;
   void* Y;
-  long long ldy, y_batch;          // elements
-  long long a_tiles, a_chunks;     // scale tiles of one matrix of A; chunks of a tile
-  long long b_tiles, b_chunks;     // scale tiles of all of B
-  int M, N, depth, groups, ragged, mt, nt;  // tiles of M; of N (unless ragged rows)
-  int steps;                       // products of 64 over the whole depth (unless ragged depth)
-  int dtype, transposed, act;
+  long long ldy, y_batch;  // elements
+  int a_batched, a_rows;
+  int depth, groups, ragged;
+  int pt, qt;       // tiles of P and Q (of the side that is not ragged, and of both else)
+  int steps;        // products of 64 over the whole depth (unless ragged depth)
+  int split;        // CTAs that share a tile's depth
+  int dtype, act;
+  int q_major;      // Y is [Q][P]: lanes along a row of Y
+  int bias_q;       // the bias goes along Q
+  int align;        // 32, 16 or less: alignment of Y's rows
   int* status;
 };
 
-template <int FMT, int BN>
+constexpr int kMaxSplit = 8;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiCols = 16;  // columns that an epilogue warp takes at a time
+constexpr int kEpiTile = 32 * 128;  // its staging tile: 32 rows of 128 bytes
+constexpr int kEpiBytes = kEpiWarps * kEpiTile;
+
+template <int FMT, int BN, bool PAIR>
 struct MmCfg {
   static constexpr int kChunkDepth = 4 * fp4_block(FMT);
   static constexpr int kChunks = kStageDepth / kChunkDepth;  // scale chunks a stage
-  static constexpr int kBTiles = BN > 128 ? 2 : 1;           // scale tiles of a B tile
-  static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = BN * 128;
+  static constexpr int kQTiles = BN > 128 ? 2 : 1;           // scale tiles of a Q tile
+  static constexpr int kPBytes = 128 * 128;
+  static constexpr int kPRows = PAIR ? 256 : 128;            // rows of a P tile
+  static constexpr int kQBytes = (PAIR ? BN / 2 : BN) * 128; // a pair holds half of Q in each CTA
   static constexpr int kSfTile = kChunks * kFp4ChunkBytes;
-  static constexpr int kSfBytes = (1 + kBTiles) * kSfTile;
-  static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-  static constexpr int kSfCols = kChunks * 4 * (1 + kBTiles);
-  static constexpr int kAccBufs = BN <= 128 ? 2 : 1;
+  static constexpr int kSfBytes = (1 + kQTiles) * kSfTile;
+  static constexpr int kStageBytes = kPBytes + kQBytes + kSfBytes;
+  static constexpr int kAccBufs = BN <= 192 ? 2 : 1;
   static constexpr int kAccCols = BN;
-  static constexpr int kStagesSmem = 221 * 1024 / kStageBytes;
-  static constexpr int kStagesTmem = (512 - kAccBufs * kAccCols) / kSfCols;
-  static constexpr int kStagesRaw = kStagesSmem < kStagesTmem ? kStagesSmem : kStagesTmem;
+  static constexpr int kSfCols = kChunks * 4 * (1 + kQTiles);
+  // 1024 for alignment, 256 of barriers, the table of groups
+  static constexpr size_t kOtherBytes = 1024 + kEpiBytes + 256 + (kFp4MaxGroups + 1) * 4;
+  static constexpr int kStagesRaw = (int)((227 * 1024 - kOtherBytes) / kStageBytes);
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
-  static_assert(kStages >= 2, "stages");
-  static_assert(kAccBufs * kAccCols + kStages * kSfCols <= 512, "tensor memory");
-  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 256 +
-                                       (kFp4MaxGroups + 1) * 4;
+  static constexpr int kSlotsRaw = (512 - kAccBufs * kAccCols) / kSfCols;
+  static constexpr int kSlots = kSlotsRaw > kStages ? kStages : kSlotsRaw;
+  static_assert(kStages >= 2 && kSlots >= 2, "stages");
+  static constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kOtherBytes;
 };
-constexpr int kMmThreads = 192;
+constexpr int kMmThreads = 64 + 32 * kEpiWarps;
 
 // One tile of work.
 struct Tile {
-  int e;         // expert (matrix of A's batch), 0 without groups
-  int m0;        // first row of A
-  int n0, nlen;  // first row of B (its own row number) and how many rows count
-  long long sb_tile;  // scale tile of B's first row
-  int sb_shift;  // place of that row in the tile (0 or 64)
-  long long k0;  // first stored depth
-  int steps;     // products of 64
+  int e;                       // expert, 0 without groups
+  int p_row, q_row;            // first rows among all stored rows of P and Q
+  int p_len, q_len;            // rows that count
+  int p_out, q_out;            // their places in Y
+  long long p_tile, q_tile;    // scale tiles of the first rows
+  int q_shift;                 // place of Q's first row in its scale tile (0 or 64)
+  long long k0;                // first stored depth
+  int steps;                   // products of 64
 };
 
-// cum: ragged rows: B tiles before each group
-template <int BN>
-__device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t) {
+// cum: ragged rows: tiles of the ragged side before each group
+// PR: rows of a P tile (128, or 256 of which rank 1 of a pair takes the upper half)
+template <int BN, int PR>
+__device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t, int pr) {
   Tile r;
   r.k0 = 0;
   r.steps = a.steps;
-  const int m = t % a.mt, u = t / a.mt;
-  r.m0 = m * 128;
+  int pi, qi;  // tile indexes of P and Q
   if (a.ragged == HINM_RAGGED_ROWS) {
+    // tiles of one ragged tile stay together: its tokens are read once
+    const int other = a.p.ragged ? a.qt : a.pt;
+    const int u = t / other, v = t - u * other;
     int lo = 0, hi = a.groups - 1;  // the last group with cum[e] <= u: empty ones share a start
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cum[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
-    const int o = __ldg(a.offsets + lo), end = __ldg(a.offsets + lo + 1);
-    const int j = (u - cum[lo]) * BN;
     r.e = lo;
-    r.n0 = o + j;
-    r.nlen = min(BN, end - r.n0);
-    r.sb_tile = fp4_group_tile(o, lo) + j / kFp4RowTile;
-    r.sb_shift = j % kFp4RowTile;
+    pi = a.p.ragged ? u - cum[lo] : v;
+    qi = a.p.ragged ? v : u - cum[lo];
   } else {
-    r.e = u / a.nt;
-    r.n0 = (u - r.e * a.nt) * BN;
-    r.nlen = min(BN, a.N - r.n0);
-    r.sb_tile = r.n0 / kFp4RowTile;
-    r.sb_shift = r.n0 % kFp4RowTile;
-    if (a.ragged == HINM_RAGGED_DEPTH) {
-      const int o = __ldg(a.offsets + r.e), end = __ldg(a.offsets + r.e + 1);
-      r.k0 = fp4_group_tile(o, r.e) * kFp4DepthPad;
-      r.steps = (end - o + kFp4DepthPad - 1) / kFp4DepthPad * 2;
-    }
+    const int per = a.pt * a.qt;
+    r.e = t / per;
+    t -= r.e * per;
+    pi = t % a.pt;
+    qi = t / a.pt;
+  }
+  int o = 0, end = 0;
+  if (a.ragged != HINM_RAGGED_NONE) {
+    o = __ldg(a.offsets + r.e);
+    end = __ldg(a.offsets + r.e + 1);
+  }
+  const int p = pi * PR + pr * 128, q = qi * BN;
+  r.q_shift = q % kFp4RowTile;
+  if (a.p.ragged) {
+    r.p_row = r.p_out = o + p;
+    r.p_len = min(128, end - r.p_row);
+    r.p_tile = fp4_group_tile(o, r.e) + p / 128;
+  } else {
+    const int m = a.p.batched ? r.e : 0;
+    r.p_row = m * a.p.rows + p;
+    r.p_out = p;
+    r.p_len = min(128, a.p.rows - p);
+    r.p_tile = m * a.p.tiles + p / 128;
+  }
+  if (a.q.ragged) {
+    r.q_row = r.q_out = o + q;
+    r.q_len = min(BN, end - r.q_row);
+    r.q_tile = fp4_group_tile(o, r.e) + q / kFp4RowTile;
+  } else {
+    const int m = a.q.batched ? r.e : 0;
+    r.q_row = m * a.q.rows + q;
+    r.q_out = q;
+    r.q_len = min(BN, a.q.rows - q);
+    r.q_tile = m * a.q.tiles + q / kFp4RowTile;
+  }
+  if (a.ragged == HINM_RAGGED_DEPTH) {
+    r.k0 = fp4_group_tile(o, r.e) * kFp4DepthPad;
+    r.steps = (end - o + kFp4DepthPad - 1) / kFp4DepthPad * 2;
   }
   return r;
 }
 
-__device__ __forceinline__ float activate(float x, int act) {
-  if (act == HINM_ACT_RELU) return fmaxf(x, 0.0f);
-  if (act == HINM_ACT_SILU) return x / (1.0f + expf(-x));
-  if (act == HINM_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == HINM_ACT_RELU) return fmaxf(x, 0.0f);
+  // (2 units in the last place; a correctly rounded division branches, element by element)
+  if constexpr (ACT == HINM_ACT_SILU) return __fdividef(x, 1.0f + expf(-x));
+  if constexpr (ACT == HINM_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
   return x;
 }
-
-__device__ __forceinline__ void store_one(const MmArgs& a, long long at, float v) {
-  if (a.dtype == HINM_DTYPE_F32) reinterpret_cast<float*>(a.Y)[at] = v;
-  else if (a.dtype == HINM_DTYPE_BF16)
-    reinterpret_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(v);
-  else reinterpret_cast<__half*>(a.Y)[at] = __float2half_rn(v);
+__device__ __forceinline__ float activate(float x, int act) {
+  switch (act) {
+    case HINM_ACT_RELU: return activate<HINM_ACT_RELU>(x);
+    case HINM_ACT_SILU: return activate<HINM_ACT_SILU>(x);
+    case HINM_ACT_GELU: return activate<HINM_ACT_GELU>(x);
+    default: return x;
+  }
+}
+// a lane's columns; the kind of activation is asked once for all of them
+template <int ACT>
+__device__ __forceinline__ void activate_all(float (&y)[kEpiCols]) {
+#pragma unroll
+  for (int i = 0; i < kEpiCols; ++i) y[i] = activate<ACT>(y[i]);
 }
 
-template <int FMT, int BN>
+__device__ __forceinline__ void store_one(void* Y, int dtype, long long at, float v) {
+  if (dtype == HINM_DTYPE_F32) reinterpret_cast<float*>(Y)[at] = v;
+  else if (dtype == HINM_DTYPE_BF16)
+    reinterpret_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(v);
+  else reinterpret_cast<__half*>(Y)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Alignment (32, 16 or 0) of Y's elements `at`, `at + ldy`, ... (its rows are `a.align`ed)
+__device__ __forceinline__ int align_of(const MmArgs& a, long long at) {
+  const int here = (int)(at * (a.dtype == HINM_DTYPE_F32 ? 4 : 2)) & 31;
+  return here == 0 ? a.align : (here & 15) == 0 ? min(a.align, 16) : 0;
+}
+
+// The tensor-core instructions, of one CTA or of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR) ptx::tc_cp_32x128b_x4_pair(taddr, desc);
+  else ptx::tc_cp_32x128b_x4(taddr, desc);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR) ptx::tc_commit_pair(bar);
+  else ptx::tc_commit(bar);
+}
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void product(uint32_t acc, uint64_t pd, uint64_t qd, uint32_t idesc,
+                                        uint32_t sfp, uint32_t sfq, uint32_t more) {
+  if constexpr (FMT == HINM_FP4_NV && PAIR)
+    ptx::mma_fp4_block16_pair(acc, pd, qd, idesc, sfp, sfq, more);
+  else if constexpr (FMT == HINM_FP4_NV)
+    ptx::mma_fp4_block16(acc, pd, qd, idesc, sfp, sfq, more);
+  else if constexpr (PAIR)
+    ptx::mma_fp4_block32_pair(acc, pd, qd, idesc, sfp, sfq, more);
+  else
+    ptx::mma_fp4_block32(acc, pd, qd, idesc, sfp, sfq, more);
+}
+
+// The warp's staging tile holds 32 rows of up to 128 bytes of Y in 16-byte pieces, piece p of row
+// r at place p ^ (r & 7): neither a lane's writes to its row nor the reads of whole rows meet in a
+// bank.
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int p) {
+  return tile + r * 128 + ((p ^ (r & 7)) << 4);
+}
+
+// A lane's 16 columns, from column c (a multiple of 16) of the staging tile on, in Y's type.
+__device__ __forceinline__ void stage(uint32_t tile, int lane, int c, int dtype,
+                                      const float (&y)[kEpiCols]) {
+  if (dtype == HINM_DTYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ptx::st_shared_v4(piece(tile, lane, c / 4 + i), __float_as_uint(y[4 * i]),
+                        __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                        __float_as_uint(y[4 * i + 3]));
+  } else {
+    uint32_t u[8];
+    if (dtype == HINM_DTYPE_BF16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = pack_f16(y[2 * i], y[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ptx::st_shared_v4(piece(tile, lane, c / 8 + i), u[4 * i], u[4 * i + 1], u[4 * i + 2],
+                        u[4 * i + 3]);
+  }
+}
+
+// The staging tile's first n columns of `rows` rows to Y, from element `at0` on.
+__device__ __forceinline__ void write_tile(const MmArgs& a, uint32_t tile, int lane, int rows,
+                                           int n, long long at0) {
+  const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
+  const int align = align_of(a, at0);
+  char* y0 = reinterpret_cast<char*>(a.Y) + at0 * es;
+  const long long pitch = a.ldy * es;
+  if (align >= 32 && n * es % 32 == 0) {
+    // 32 bytes a lane, a row's 128 in four lanes
+    const int p = (lane & 3) * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      if (r < rows && p * 16 < n * es) {
+        const uint4 u = ptx::ld_shared_v4(piece(tile, r, p));
+        const uint4 v = ptx::ld_shared_v4(piece(tile, r, p + 1));
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         y0 + r * pitch + p * 16),
+                     "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+      }
+    }
+  } else if (align >= 16 && n * es % 16 == 0) {
+    const int p = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      if (r < rows && p * 16 < n * es)
+        *reinterpret_cast<uint4*>(y0 + r * pitch + p * 16) = ptx::ld_shared_v4(piece(tile, r, p));
+    }
+  } else {
+    // rows that start anywhere: element by element, lanes along a row
+#pragma unroll 4
+    for (int r = 0; r < min(rows, 32); ++r) {
+      for (int c = lane; c < n; c += 32) {
+        const uint32_t from = piece(tile, r, c * es / 16) + c * es % 16;
+        if (es == 4) {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+          *reinterpret_cast<uint32_t*>(y0 + r * pitch + c * 4) = v;
+        } else {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
+          *reinterpret_cast<uint16_t*>(y0 + r * pitch + c * 2) = v;
+        }
+      }
+    }
+  }
+}
+
+// COLS columns of whole 32-byte aligned rows of Y: what a tile inside Y takes.  Lane l brings row l
+// of the accumulator at `acc`; all of its columns are read first, and `done` is called, so that the
+// accumulator is free while they are worked on, PC of them (64 or 128 bytes) at a time.  rows: how
+// many count; y: element 0 of row 0 of Y.
+template <int DT, int COLS, bool BIASQ, class Done>
+__device__ __forceinline__ void write_columns(const MmArgs& a, uint32_t acc, bool zero, float alpha,
+                                              float bias_row, const float* bias_cols,
+                                              uint32_t tile, int lane, int rows, char* y,
+                                              Done done) {
+  constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
+  constexpr int PC = DT != HINM_DTYPE_F32 && COLS % 64 == 0 ? 64 : 32;
+  constexpr int kLanes = PC * es / 32;  // lanes that write one row, 32 bytes each
+  constexpr int kRows = 32 / kLanes;    // rows of one store
+  uint32_t v[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS; i += 32) {
+    if (!zero) {
+      ptx::tmem_ld_32x32b_x32(acc + i, reinterpret_cast<uint32_t(&)[32]>(v[i]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[i + j] = 0;
+    }
+  }
+  ptx::tmem_ld_wait();
+  done();
+  // places in the staging tile (piece()): of this lane's row, and of what it writes out (a row's
+  // number mod 8 does not change from store to store)
+  const uint32_t in = tile + lane * 128 + ((lane & 7) << 4);
+  const int r0 = lane / kLanes, p0 = (lane % kLanes) * 2;
+  const uint32_t out = tile + r0 * 128 + ((p0 ^ (r0 & 7)) << 4);
+  const long long pitch = a.ldy * es;
+  char* yr = y + r0 * pitch + p0 * 16;
+#pragma unroll
+  for (int col = 0; col < COLS; col += PC) {
+#pragma unroll
+    for (int h = 0; h < PC; h += kEpiCols) {
+      float f[kEpiCols];
+#pragma unroll
+      for (int i = 0; i < kEpiCols; ++i)
+        f[i] = fmaf(__uint_as_float(v[col + h + i]), alpha,
+                    BIASQ ? __ldg(bias_cols + col + h + i) : bias_row);
+      if (a.act == HINM_ACT_NONE) {
+      } else if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU>(f);
+      else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU>(f);
+      else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU>(f);
+#pragma unroll
+      for (int i = 0; i < kEpiCols * es / 16; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          u[j] = DT == HINM_DTYPE_F32    ? __float_as_uint(f[4 * i + j])
+                 : DT == HINM_DTYPE_BF16 ? pack_bf16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1])
+                                         : pack_f16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1]);
+        ptx::st_shared_v4(in ^ (uint32_t)(h * es + 16 * i), u[0], u[1], u[2], u[3]);
+      }
+    }
+    __syncwarp();
+    char* yo = yr + col * es;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) {
+      if (r0 + i * kRows < rows) {
+        const uint4 u = ptx::ld_shared_v4(out + i * kRows * 128);
+        const uint4 w = ptx::ld_shared_v4((out ^ 16) + i * kRows * 128);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(yo), "r"(u.x),
+                     "r"(u.y), "r"(u.z), "r"(u.w), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                     : "memory");
+      }
+      yo += kRows * pitch;
+    }
+    __syncwarp();
+  }
+}
+
+// Four consecutive elements of Y, n of them real, from element `at` on.
+__device__ __forceinline__ void store_four(const MmArgs& a, const float (&y)[4], int n,
+                                           long long at) {
+  const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
+  if (n >= 4 && a.align >= 16 && (at * es) % (4 * es) == 0) {
+    if (a.dtype == HINM_DTYPE_F32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.Y) + at) =
+          make_float4(y[0], y[1], y[2], y[3]);
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + at) =
+          a.dtype == HINM_DTYPE_BF16
+              ? make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]))
+              : make_uint2(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < n) store_one(a.Y, a.dtype, at + q, y[q]);
+  }
+}
+
+template <int FMT, int BN, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(kMmThreads, 1)
-    fp4_mm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    fp4_mm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                  const __grid_constant__ CUtensorMap tmSp, const __grid_constant__ CUtensorMap tmSq,
                   const MmArgs a) {
-  using C = MmCfg<FMT, BN>;
+  static_assert(!(SPLIT && PAIR), "a cluster has one use");
+  using C = MmCfg<FMT, BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
-  ptx::enter_dependent();
+  if constexpr (PAIR) ptx::enter_dependent();
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint8_t* epi_smem = smem + C::kStages * C::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_smem + kEpiBytes);
   // [0,S) full, [S,2S) empty, 2S+{0,1} accumulator full, 2S+{2,3} accumulator empty, 2S+4 drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* bad_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int* cum = reinterpret_cast<int*>(smem + C::kStages * C::kStageBytes + 256);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* cum = reinterpret_cast<int*>(epi_smem + kEpiBytes + 256);
+  // the same in every lane, and known to be
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   auto full_bar = [&](int s) { return ptx::smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return ptx::smem_u32(bars + C::kStages + s); };
   auto accf_bar = [&](int b) { return ptx::smem_u32(bars + 2 * C::kStages + b); };
@@ -167,7 +463,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar(b), 1);
-      ptx::mbar_init(acce_bar(b), 4);
+      ptx::mbar_init(acce_bar(b), (PAIR ? 2 : 1) * kEpiWarps);
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -175,23 +471,34 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish();
-  }
-  __syncthreads();
-  // offsets that decrease or leave the matrix are reported, and nothing is computed
-  if (a.ragged != HINM_RAGGED_NONE) {
-    const int limit = a.ragged == HINM_RAGGED_ROWS ? a.N : a.depth;
-    for (int e = threadIdx.x; e < a.groups; e += kMmThreads) {
-      const int o = __ldg(a.offsets + e), end = __ldg(a.offsets + e + 1);
-      if (o < 0 || end < o || end > limit) *bad_flag = 1;
+    if constexpr (PAIR) {
+      ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+    } else {
+      ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+      ptx::tmem_relinquish();
     }
-    if (a.ragged == HINM_RAGGED_ROWS && warp == 0) {
+  }
+  if (lane == 0) {
+    if (warp == 2) ptx::prefetch_map(&tmP);
+    if (warp == 3) ptx::prefetch_map(&tmQ);
+    if (PAIR && warp == 4) ptx::prefetch_map(&tmSp);
+    if (PAIR && warp == 5) ptx::prefetch_map(&tmSq);
+  }
+  // What is above touches no global memory: it runs while the stream's previous kernel ends.
+  if constexpr (!PAIR) ptx::enter_dependent();
+  if (warp == 0) {
+    if (a.ragged != HINM_RAGGED_NONE) {
+      // offsets that decrease or leave the matrix are reported, and nothing is computed
+      const int limit = a.ragged == HINM_RAGGED_DEPTH ? a.depth : a.p.ragged ? a.p.rows : a.q.rows;
+      const int per = a.p.ragged ? C::kPRows : BN;
       int before = 0;
+      bool bad = false;
       for (int base = 0; base < a.groups; base += 32) {
         const int e = base + lane;
-        int n = e < a.groups ? __ldg(a.offsets + e + 1) - __ldg(a.offsets + e) : 0;
-        n = n > 0 ? (n + BN - 1) / BN : 0;
+        const int o = e < a.groups ? __ldg(a.offsets + e) : 0;
+        const int end = e < a.groups ? __ldg(a.offsets + e + 1) : 0;
+        bad |= o < 0 || end < o || end > limit;
+        const int n = end > o ? (end - o + per - 1) / per : 0;
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -201,58 +508,108 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (e < a.groups) cum[e] = before + sum - n;
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
       }
-      if (lane == 0) cum[a.groups] = before;
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (lane == 0) {
+        cum[a.groups] = before;
+        if (bad) {
+          *bad_flag = 1;
+          ptx::record_status(a.status, HINM_ERR_INVALID_ARG);
+        }
+      }
     }
+    __syncwarp();
   }
   ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  int tiles = a.ragged == HINM_RAGGED_ROWS   ? cum[a.groups] * a.mt
-              : a.ragged == HINM_RAGGED_DEPTH ? a.groups * a.nt * a.mt
-                                              : a.nt * a.mt;
-  if (*bad_flag) {
-    if (threadIdx.x == 0) ptx::record_status(a.status, HINM_ERR_INVALID_ARG);
-    tiles = 0;
+  if constexpr (PAIR) {
+    ptx::cluster_sync();  // the barriers of both CTAs stand
+  } else if (warp == 0) {
+    // the copies need nothing of the other warps: they start while tensor memory is allocated
+    asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kMmThreads) : "memory");
+  } else {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(kMmThreads) : "memory");
   }
-  const uint32_t sf_col0 = C::kAccBufs * C::kAccCols;
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // not read by warp 0
+  int tiles = a.pt * a.qt;
+  if (a.ragged == HINM_RAGGED_ROWS) tiles = cum[a.groups] * (a.p.ragged ? a.qt : a.pt);
+  if (a.ragged == HINM_RAGGED_DEPTH) tiles = a.groups * a.pt * a.qt;
+  if (*bad_flag) tiles = 0;
+  // SPLIT, Y as [P][Q]: row pitch of the partial sums, an odd number of 16-byte pieces
+  constexpr int kPartRow = BN + 4;
+  static_assert(!SPLIT || 128 * kPartRow * 4 <= C::kStages * C::kStageBytes, "partial sums");
+  constexpr uint32_t kSfCol0 = C::kAccBufs * C::kAccCols;
+  // SPLIT: a cluster takes one tile, rank r the stages [n r / split, n (r + 1) / split)
+  // PAIR: a cluster of two takes a tile of 256 rows of P, rank r rows 128 r .. 128 r + 127
+  const int first = SPLIT ? (int)blockIdx.x / a.split : PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
+  const int step = SPLIT ? 0x40000000 : PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
+  const int rank = SPLIT ? (int)blockIdx.x % a.split : PAIR ? (int)blockIdx.x % 2 : 0;
+  auto tile_at = [&](int t) { return tile_of<BN, C::kPRows>(a, cum, t, PAIR ? rank : 0); };
+  // columns of a tile's products: a pair's halves are whole groups of 16
+  auto mma_n = [](int q_len) { return PAIR ? (q_len + 31) & ~31 : (q_len + 15) & ~15; };
+  auto stage_range = [&](int steps, int& s0, int& s1) {
+    const int n = (steps + 3) / 4;
+    s0 = SPLIT ? n * rank / a.split : 0;
+    s1 = SPLIT ? n * (rank + 1) / a.split : n;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     if (lane == 0) {
       uint32_t it = 0;
       bool stop = false;
-      for (int t = blockIdx.x; t < tiles && !stop; t += gridDim.x) {
-        const Tile w = tile_of<BN>(a, cum, t);
-        const int batch = a.ragged == HINM_RAGGED_DEPTH ? 0 : w.e;  // matrix of A
-        const uint8_t* sa = a.sa + ((batch * a.a_tiles + w.m0 / 128) * a.a_chunks +
-                                    w.k0 / C::kChunkDepth) * kFp4ChunkBytes;
-        const uint8_t* sb = a.sb + (w.sb_tile * a.b_chunks + w.k0 / C::kChunkDepth) * kFp4ChunkBytes;
-        const int a_row = batch * a.M + w.m0;
-        const bool two = C::kBTiles == 2 && w.nlen > 128;  // B's second scale tile exists
-        for (int st = 0; st < w.steps; st += 4, ++it) {
+      for (int t = first; t < tiles && !stop; t += step) {
+        const Tile w = tile_at(t);
+        const long long c0 = w.k0 / C::kChunkDepth;
+        const uint8_t* sp = a.p.scales + (w.p_tile * a.p.chunks + c0) * kFp4ChunkBytes;
+        const uint8_t* sq = a.q.scales + (w.q_tile * a.q.chunks + c0) * kFp4ChunkBytes;
+        const bool two = C::kQTiles == 2 && w.q_shift + w.q_len > kFp4RowTile;
+        const int pb = (w.p_len + kBoxRows - 1) / kBoxRows;
+        const int qb = (w.q_len + kBoxRows - 1) / kBoxRows;
+        int s0, s1;
+        stage_range(w.steps, s0, s1);
+        for (int st = s0; st < s1; ++st, ++it) {
           const int s = it % C::kStages;
           if (!ptx::mbar_wait(empty_bar(s), ((it / C::kStages) & 1) ^ 1, a.status, abort_flag)) {
             stop = true;
             break;
           }
-          const int left = min(4, w.steps - st);
+          const int left = min(4, w.steps - 4 * st);
           const uint32_t sf = (uint32_t)(left * 64 / C::kChunkDepth) * kFp4ChunkBytes;
-          const uint32_t A_s = ptx::smem_u32(smem + s * C::kStageBytes);
-          const uint32_t B_s = A_s + C::kABytes, S_s = B_s + C::kBBytes;
-          ptx::mbar_arrive_expect_tx(full_bar(s), C::kABytes + C::kBBytes + sf * (two ? 3 : 2));
-          const int x = (int)(w.k0 / 2) + st * 32;
-          ptx::tma_load_2d(A_s, &tmA, x, a_row, full_bar(s));
-          ptx::tma_load_2d(B_s, &tmB, x, w.n0, full_bar(s));
-          const long long at = (long long)(st * 64 / C::kChunkDepth) * kFp4ChunkBytes;
-          ptx::bulk_g2s(S_s, sa + at, sf, full_bar(s));
-          ptx::bulk_g2s(S_s + C::kSfTile, sb + at, sf, full_bar(s));
+          const uint32_t P_s = ptx::smem_u32(smem + s * C::kStageBytes);
+          const uint32_t Q_s = P_s + C::kPBytes, S_s = Q_s + C::kQBytes;
+          if constexpr (PAIR) {
+            // whole stages in both CTAs (what a partial tile does not need goes unread), all
+            // completing on rank 0's barrier; scales as boxes of the stage's chunks
+            const uint32_t bar = ptx::mapa_shared(full_bar(s), 0);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * C::kStageBytes);
+            const int x = (int)(w.k0 / 2) + st * 128, q_row = w.q_row + rank * (mma_n(w.q_len) / 2);
+            const int c = (int)c0 + st * C::kChunks;
+            for (int b = 0; b < 2; ++b) {
+              ptx::tma_load_2d_pair(P_s + b * kBoxRows * 128, &tmP, x, w.p_row + b * kBoxRows, bar);
+              ptx::tma_load_2d_pair(Q_s + b * kBoxRows * 128, &tmQ, x, q_row + b * kBoxRows, bar);
+            }
+            ptx::tma_load_2d_pair(S_s, &tmSp, 0, (int)(w.p_tile * a.p.chunks) + c, bar);
+            for (int j = 0; j < 2; ++j)
+              ptx::tma_load_2d_pair(S_s + (1 + j) * C::kSfTile, &tmSq, 0,
+                                    (int)((w.q_tile + j) * a.q.chunks) + c, bar);
+            continue;
+          }
+          ptx::mbar_arrive_expect_tx(full_bar(s), (uint32_t)(pb + qb) * (kBoxRows * 128) +
+                                                      sf * (two ? 3 : 2));
+          const int x = (int)(w.k0 / 2) + st * 128;
+          for (int b = 0; b < pb; ++b)
+            ptx::tma_load_2d(P_s + b * kBoxRows * 128, &tmP, x, w.p_row + b * kBoxRows, full_bar(s));
+          for (int b = 0; b < qb; ++b)
+            ptx::tma_load_2d(Q_s + b * kBoxRows * 128, &tmQ, x, w.q_row + b * kBoxRows, full_bar(s));
+          const long long at = (long long)st * C::kSfTile;
+          ptx::bulk_g2s(S_s, sp + at, sf, full_bar(s));
+          ptx::bulk_g2s(S_s + C::kSfTile, sq + at, sf, full_bar(s));
           if (two)
-            ptx::bulk_g2s(S_s + 2 * C::kSfTile, sb + a.b_chunks * kFp4ChunkBytes + at, sf,
+            ptx::bulk_g2s(S_s + 2 * C::kSfTile, sq + a.q.chunks * kFp4ChunkBytes + at, sf,
                           full_bar(s));
         }
       }
-      if (*abort_flag) {
+      if (*abort_flag && !(PAIR && rank != 0)) {
         for (uint32_t k = it > (uint32_t)C::kStages ? it - C::kStages : 0u; k < it; ++k)
           ptx::mbar_wait(full_bar(k % C::kStages), (k / C::kStages) & 1, a.status, nullptr);
       }
@@ -260,107 +617,267 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      uint32_t it = 0, lu = 0;
-      bool stop = false;
-      for (int t = blockIdx.x; t < tiles && !stop; t += gridDim.x, ++lu) {
-        const Tile w = tile_of<BN>(a, cum, t);
-        const int b = (int)(lu % C::kAccBufs);
-        if (!ptx::mbar_wait(acce_bar(b), ((lu / C::kAccBufs) & 1) ^ 1, a.status, abort_flag)) break;
-        ptx::tc_fence_after();
-        const uint32_t acc = tmem + b * C::kAccCols;
-        const int n = (w.nlen + 15) & ~15;
-        const uint32_t id0 = ptx::idesc_fp4(n, FMT == HINM_FP4_MX, 0);
-        const uint32_t id2 = ptx::idesc_fp4(n, FMT == HINM_FP4_MX, 2);
-        const int tb = w.nlen > 128 ? 2 : 1;
-        for (int st = 0; st < w.steps; st += 4, ++it) {
-          const int s = it % C::kStages;
-          if (!ptx::mbar_wait(full_bar(s), (it / C::kStages) & 1, a.status, abort_flag)) {
-            stop = true;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t A_s = ptx::smem_u32(smem + s * C::kStageBytes);
-          const uint32_t B_s = A_s + C::kABytes, S_s = B_s + C::kBBytes;
-          const uint32_t sf = tmem + sf_col0 + s * C::kSfCols;
-          const int left = min(4, w.steps - st);
-          const int chunks = left * 64 / C::kChunkDepth;
-          for (int c = 0; c < chunks; ++c) {
-            // 32 rows of 16 bytes: core matrices of 8 rows, 128 bytes apart
-            ptx::tc_cp_32x128b_x4(sf + 4 * c,
-                                  ptx::smem_desc(S_s + c * kFp4ChunkBytes, 16, 128, 0));
-            for (int j = 0; j < tb; ++j)
-              ptx::tc_cp_32x128b_x4(
-                  sf + 4 * C::kChunks + 4 * C::kBTiles * c + 4 * j,
-                  ptx::smem_desc(S_s + (1 + j) * C::kSfTile + c * kFp4ChunkBytes, 16, 128, 0));
-          }
-          const uint32_t sfb = sf + 4 * C::kChunks + w.sb_shift / 32;
-          for (int k = 0; k < left; ++k) {
-            const uint64_t ad = ptx::smem_desc(A_s + 32 * k, 16, 1024, 2);
-            const uint64_t bd = ptx::smem_desc(B_s + 32 * k, 16, 1024, 2);
-            if constexpr (FMT == HINM_FP4_NV)
-              ptx::mma_fp4_block16(acc, ad, bd, id0, sf + 4 * k, sfb + 4 * C::kBTiles * k,
-                                   (st | k) ? 1u : 0u);
-            else
-              ptx::mma_fp4_block32(acc, ad, bd, (k & 1) ? id2 : id0, sf + 4 * (k / 2),
-                                   sfb + 4 * C::kBTiles * (k / 2), (st | k) ? 1u : 0u);
-          }
-          ptx::tc_commit(empty_bar(s));
+    // The whole warp walks the stages and one lane issues: a stage is 4 products and up to 12
+    // scale copies in some 500 cycles, so what is issued between them counts.  (With loops and
+    // descriptors made in the branch of one lane, 8192^3 took 678 us; in this form, 359.)
+    uint32_t it = 0, lu = 0;
+    bool stop = false;
+    // descriptors of stage 0: their upper words do not change, the address field of the lower
+    // counts 16 bytes
+    const uint32_t base = ptx::smem_u32(smem);
+    const uint64_t pd0 = ptx::smem_desc(base, 16, 1024, 2);
+    const uint64_t qd0 = ptx::smem_desc(base + C::kPBytes, 16, 1024, 2);
+    // scales: 32 rows of 16 bytes, core matrices of 8 rows 128 bytes apart
+    const uint64_t sd0 = ptx::smem_desc(base + C::kPBytes + C::kQBytes, 16, 128, 0);
+    const int mine = PAIR && rank != 0 ? 0 : tiles;  // rank 0 of a pair issues for both
+    for (int t = first; t < mine && !stop; t += step, ++lu) {
+      const Tile w = tile_at(t);
+      const int b = (int)(lu % C::kAccBufs);
+      bool ok = ptx::mbar_wait(acce_bar(b), ((lu / C::kAccBufs) & 1) ^ 1, a.status, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + b * C::kAccCols;
+      const uint32_t n = mma_n(w.q_len), q_shift = w.q_shift / 32;
+      const uint32_t id0 = ptx::idesc_fp4(C::kPRows, n, FMT == HINM_FP4_MX, 0);
+      const uint32_t id2 = ptx::idesc_fp4(C::kPRows, n, FMT == HINM_FP4_MX, 2);
+      const bool two =
+          __any_sync(0xFFFFFFFFu, C::kQTiles == 2 && w.q_shift + w.q_len > kFp4RowTile);
+      int s0, s1;
+      stage_range(w.steps, s0, s1);
+      for (int st = s0; st < s1; ++st, ++it) {
+        const uint32_t s = it % C::kStages;
+        ok = ptx::mbar_wait(full_bar(s), (it / C::kStages) & 1, a.status, abort_flag);
+        if (C::kSlots < C::kStages && it >= (uint32_t)C::kSlots) {
+          // the products that read this slot's scales are done
+          const uint32_t old = it - C::kSlots;
+          ok = ok && ptx::mbar_wait(empty_bar(old % C::kStages), (old / C::kStages) & 1, a.status,
+                                    abort_flag);
         }
-        if (stop) break;
-        ptx::tc_commit(accf_bar(b));
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          stop = true;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t off = s * (C::kStageBytes / 16);
+        const uint64_t pd = pd0 + off, qd = qd0 + off, sd = sd0 + off;
+        const uint32_t sfp = tmem + kSfCol0 + (it % C::kSlots) * C::kSfCols;
+        const uint32_t sfq = sfp + 4 * C::kChunks;
+        const uint32_t sfq_mma = sfq + q_shift;
+        const int left = min(4, w.steps - 4 * st);
+        const uint32_t more = st > s0;
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c) {
+            if (c * (C::kChunkDepth / 64) < left) {
+              scale_copy<PAIR>(sfp + 4 * c, sd + c * (kFp4ChunkBytes / 16));
+              scale_copy<PAIR>(sfq + 4 * C::kQTiles * c,
+                               sd + (C::kSfTile + c * kFp4ChunkBytes) / 16);
+              if (two)
+                scale_copy<PAIR>(sfq + 4 * C::kQTiles * c + 4,
+                                 sd + (2 * C::kSfTile + c * kFp4ChunkBytes) / 16);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < left) {
+              if constexpr (FMT == HINM_FP4_NV)
+                product<FMT, PAIR>(acc, pd + 2 * k, qd + 2 * k, id0, sfp + 4 * k,
+                                   sfq_mma + 4 * C::kQTiles * k, k > 0 ? 1u : more);
+              else
+                product<FMT, PAIR>(acc, pd + 2 * k, qd + 2 * k, (k & 1) ? id2 : id0,
+                                   sfp + 4 * (k / 2), sfq_mma + 4 * C::kQTiles * (k / 2),
+                                   k > 0 ? 1u : more);
+            }
+          }
+          commit<PAIR>(empty_bar(s));
+        }
+        __syncwarp();
       }
-      ptx::tc_commit(drain_bar);
+      if (stop) break;
+      if (ptx::elect_one()) commit<PAIR>(accf_bar(b));
+      __syncwarp();
+    }
+    if (ptx::elect_one()) {
+      if (!PAIR || rank == 0) commit<PAIR>(drain_bar);  // the last commit that reaches rank 1
       ptx::mbar_wait(drain_bar, 0, a.status, nullptr);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    const int quad = warp & 3, part = (warp - 2) >> 2;  // warps 2..5 and 6..9
+    constexpr int kOwn = BN / (kEpiWarps / 4);  // columns of this warp
+    static_assert(kOwn % kEpiCols == 0, "columns");
+    const int row = quad * 32 + lane;
+    // this warp has read what it needs of accumulator b
+    auto release = [&](int b) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(acce_bar(b), 0));
+        else ptx::mbar_arrive(acce_bar(b));
+      }
+    };
     uint32_t lu = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++lu) {
-      const Tile w = tile_of<BN>(a, cum, t);
+    for (int t = first; t < tiles; t += step, ++lu) {
+      const Tile w = tile_at(t);
       const int b = (int)(lu % C::kAccBufs);
-      bool ok = ptx::mbar_wait(accf_bar(b), (lu / C::kAccBufs) & 1, a.status, abort_flag);
+      bool ok = true;  // one lane asks, so that the waiting warps take few issue slots
+      if (lane == 0) ok = ptx::mbar_wait(accf_bar(b), (lu / C::kAccBufs) & 1, a.status, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       ptx::tc_fence_after();
-      const int m = w.m0 + q * 32 + lane;
-      const int batch = a.ragged == HINM_RAGGED_DEPTH ? 0 : w.e;  // matrix of A
-      const float alpha = (a.ga ? __ldg(a.ga + batch) : 1.0f) * (a.gb ? __ldg(a.gb) : 1.0f);
-      const float bias =
-          a.bias && m < a.M ? __ldg(a.bias + (long long)batch * a.M + m) : 0.0f;
+      int s0, s1;
+      stage_range(w.steps, s0, s1);
+      const int m = a.a_batched ? w.e : 0;
+      const float alpha = (a.ga ? __ldg(a.ga + m) : 1.0f) * (a.gb ? __ldg(a.gb) : 1.0f);
+      const float* bias = a.bias ? a.bias + (long long)m * a.a_rows : nullptr;
+      const bool mine = row < w.p_len;
+      const float bias_p = bias && !a.bias_q && mine ? __ldg(bias + w.p_out + row) : 0.0f;
       const long long y0 = a.ragged == HINM_RAGGED_DEPTH ? w.e * a.y_batch : 0;
-      for (int col = 0; col < w.nlen; col += 32) {
-        uint32_t v[32];
-        if (w.steps > 0) {
-          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::kAccCols + col);
-          ptx::tmem_ld_32x32b_x32(at, v);
-          ptx::tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0;
+      const int col0 = part * kOwn, col1 = min(w.q_len, col0 + kOwn);
+      const uint32_t tile = ptx::smem_u32(epi_smem + (warp - 2) * kEpiTile);
+      const int pass = a.dtype == HINM_DTYPE_F32 ? 32 : 64;  // columns of the staging tile
+      const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * C::kAccCols);
+      if constexpr (!SPLIT) {
+        const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
+        const long long at0 = y0 + (long long)(w.p_out + quad * 32) * a.ldy + w.q_out + col0;
+        if (!a.q_major && w.q_len == BN && align_of(a, at0) == 32) {
+          const float* bias_cols = bias && a.bias_q ? bias + w.q_out + col0 : nullptr;
+          char* y = reinterpret_cast<char*>(a.Y) + at0 * es;
+          const int rows = w.p_len - quad * 32;
+          auto done = [&] { release(b); };
+          auto write = [&](auto dt) {
+            constexpr int DT = decltype(dt)::value;
+            if (bias_cols)
+              write_columns<DT, kOwn, true>(a, lanes + col0, s1 == s0, alpha, bias_p, bias_cols,
+                                            tile, lane, rows, y, done);
+            else
+              write_columns<DT, kOwn, false>(a, lanes + col0, s1 == s0, alpha, bias_p, nullptr,
+                                             tile, lane, rows, y, done);
+          };
+          if (a.dtype == HINM_DTYPE_BF16) write(std::integral_constant<int, HINM_DTYPE_BF16>{});
+          else if (a.dtype == HINM_DTYPE_F16) write(std::integral_constant<int, HINM_DTYPE_F16>{});
+          else write(std::integral_constant<int, HINM_DTYPE_F32>{});
+          continue;
         }
-        if (m < a.M) {
+      }
+      uint32_t next[kEpiCols];
+      if (col0 < col1 && s1 > s0) {
+        ptx::tmem_ld_16(lanes + col0, next);
+        ptx::tmem_ld_wait();
+      }
+#pragma unroll 1
+      for (int col = col0; col < col1; col += kEpiCols) {
+        uint32_t v[kEpiCols];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (col + i < w.nlen) {
-              const float y = activate(fmaf(__uint_as_float(v[i]), alpha, bias), a.act);
-              const long long n = w.n0 + col + i;
-              store_one(a, y0 + (a.transposed ? n * a.ldy + m : (long long)m * a.ldy + n), y);
+        for (int i = 0; i < kEpiCols; ++i) v[i] = s1 > s0 ? next[i] : 0u;  // no depth: zeros
+        const bool last = col + kEpiCols >= col1;
+        // the next columns arrive while these are worked on
+        if (!last && s1 > s0) ptx::tmem_ld_16(lanes + col + kEpiCols, next);
+        if (last) release(b);
+        const int n = min(kEpiCols, w.q_len - col);
+        if constexpr (SPLIT) {
+          // partial sums to this CTA's stages, which its products are done with, in Y's order
+          if (a.q_major) {
+            float* part_sums = reinterpret_cast<float*>(smem) + col * 128 + row;
+#pragma unroll
+            for (int i = 0; i < kEpiCols; ++i)
+              if (i < n) part_sums[i * 128] = __uint_as_float(v[i]);
+          } else {
+            uint4* part_sums = reinterpret_cast<uint4*>(smem + (row * kPartRow + col) * 4);
+#pragma unroll
+            for (int i = 0; i < kEpiCols / 4; ++i)
+              part_sums[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        } else {
+          float y[kEpiCols];
+          if (bias && a.bias_q) {
+#pragma unroll
+            for (int i = 0; i < kEpiCols; ++i)
+              y[i] = fmaf(__uint_as_float(v[i]), alpha,
+                          i < n ? __ldg(bias + w.q_out + col + i) : 0.0f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kEpiCols; ++i) y[i] = fmaf(__uint_as_float(v[i]), alpha, bias_p);
+          }
+          if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU>(y);
+          else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU>(y);
+          else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU>(y);
+          if (a.q_major) {
+#pragma unroll
+            for (int i = 0; i < kEpiCols; ++i)
+              if (i < n && mine)
+                store_one(a.Y, a.dtype,
+                          y0 + (long long)(w.q_out + col + i) * a.ldy + w.p_out + row, y[i]);
+          } else {
+            const int c = (col - col0) & (pass - 1);
+            stage(tile, lane, c, a.dtype, y);
+            if (last || c + kEpiCols == pass) {
+              __syncwarp();
+              write_tile(a, tile, lane, w.p_len - quad * 32, c + n,
+                         y0 + (long long)(w.p_out + quad * 32) * a.ldy + w.q_out + col - c);
+              __syncwarp();
             }
           }
         }
+        if (!last && s1 > s0) ptx::tmem_ld_wait();
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(acce_bar(b));
+      if (col0 >= col1) release(b);  // none of the columns
     }
   }
+  if constexpr (SPLIT) {
+    ptx::cluster_sync();  // every CTA's partial sums are in its shared memory
+    if (first < tiles && !*abort_flag) {
+      const Tile w = tile_at(first);
+      const int m = a.a_batched ? w.e : 0;
+      const float alpha = (a.ga ? __ldg(a.ga + m) : 1.0f) * (a.gb ? __ldg(a.gb) : 1.0f);
+      const float* bias = a.bias ? a.bias + (long long)m * a.a_rows : nullptr;
+      const long long y0 = a.ragged == HINM_RAGGED_DEPTH ? w.e * a.y_batch : 0;
+      // groups of 4 along Y's rows, shared out over the ranks: rows of Y are P's 128 for a
+      // column (q_major), else a row's columns
+      const int inner = a.q_major ? 32 : (w.q_len + 3) / 4;
+      const int outer = a.q_major ? w.q_len : w.p_len;
+      const int o0 = outer * rank / a.split, groups = (outer * (rank + 1) / a.split - o0) * inner;
+      const uint32_t part = ptx::smem_u32(smem);
+      for (int i = threadIdx.x; i < groups; i += kMmThreads) {
+        const int o = o0 + i / inner, j = i % inner * 4;
+        const uint32_t at = part + (uint32_t)(o * (a.q_major ? 128 : kPartRow) + j) * 4;
+        float4 v[kMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) {
+          v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (r < a.split) v[r] = ptx::ld_cluster_v4(ptx::mapa_shared(at, r));
+        }
+        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+        for (int r = 1; r < kMaxSplit; ++r) {
+          if (r < a.split) {
+            y[0] = __fadd_rn(y[0], v[r].x);
+            y[1] = __fadd_rn(y[1], v[r].y);
+            y[2] = __fadd_rn(y[2], v[r].z);
+            y[3] = __fadd_rn(y[3], v[r].w);
+          }
+        }
+        const int n = min(4, (a.q_major ? w.p_len : w.q_len) - j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int prow = w.p_out + (a.q_major ? j + q : o), qcol = w.q_out + (a.q_major ? o : j + q);
+          const float bi = bias && q < n ? __ldg(bias + (a.bias_q ? qcol : prow)) : 0.0f;
+          y[q] = activate(fmaf(y[q], alpha, bi), a.act);
+        }
+        const long long out = y0 + (a.q_major ? (long long)(w.q_out + o) * a.ldy + w.p_out + j
+                                              : (long long)(w.p_out + o) * a.ldy + w.q_out + j);
+        store_four(a, y, n, out);
+      }
+    }
+    ptx::cluster_sync();  // nobody reads this CTA's shared memory any more
+  }
   ptx::tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // nothing of the other CTA's is in flight here
+  else __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, 512);
+    else ptx::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -394,6 +911,19 @@ bool make_map(CUtensorMap* m, const uint8_t* values, long long rows, long long p
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale chunks as rows of 512 bytes, boxes of a stage's chunks, zeros past the last.
+bool make_scale_map(CUtensorMap* m, const uint8_t* scales, long long chunks, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {kFp4ChunkBytes / 4, (cuuint64_t)chunks};
+  cuuint64_t strides[1] = {kFp4ChunkBytes};
+  cuuint32_t box[2] = {kFp4ChunkBytes / 4, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(scales), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
   static int n = 0;
   if (n == 0) {
@@ -405,41 +935,127 @@ int num_sms() {
   return n;
 }
 
-template <int FMT, int BN>
-cudaError_t run(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, cudaStream_t s) {
-  using C = MmCfg<FMT, BN>;
-  cudaError_t e = set_max_dynamic_smem((const void*)fp4_mm_kernel<FMT, BN>, (int)C::kSmemBytes);
+// box_rows is 64 for every map: a tile loads as many boxes as it has rows for.
+struct Maps {
+  CUtensorMap p, q, sp, sq;  // values; scales (pairs)
+};
+
+template <int FMT, int BN, bool SPLIT, bool PAIR>
+cudaError_t run(MmArgs a, const Maps& m, long long tiles, cudaStream_t s) {
+  using C = MmCfg<FMT, BN, PAIR>;
+  auto kernel = fp4_mm_kernel<FMT, BN, SPLIT, PAIR>;
+  cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const Fp4Geom ga = fp4_geom(A.rows, A.depth, A.ragged, A.groups);
-  const Fp4Geom gb = fp4_geom(B.rows, B.depth, B.ragged, B.groups);
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, A.values, (long long)A.batch * A.rows, ga.pitch(), 128) ||
-      !make_map(&mb, B.values, B.rows, gb.pitch(), BN))
-    return cudaErrorInvalidValue;
-  a.a_tiles = ga.row_tiles;
-  a.a_chunks = ga.chunks(FMT);
-  a.b_tiles = gb.row_tiles;
-  a.b_chunks = gb.chunks(FMT);
-  a.steps = (int)(ga.depth_pad / 64);
-  a.mt = (A.rows + 127) / 128;
-  a.nt = (B.rows + BN - 1) / BN;
-  // ragged rows: no more column tiles than full ones and one partial for each group
-  const long long nt = a.ragged == HINM_RAGGED_ROWS    ? (long long)B.rows / BN + a.groups
-                       : a.ragged == HINM_RAGGED_DEPTH ? (long long)a.nt * a.groups
-                                                       : a.nt;
-  const long long tiles = nt * a.mt;
-  if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const int grid = tiles < num_sms() ? (int)tiles : num_sms();
-  return launch_kernel(fp4_mm_kernel<FMT, BN>, grid, kMmThreads, C::kSmemBytes, s, nullptr, ma, mb,
-                       a);
+  if constexpr (!SPLIT && !PAIR) {
+    const int grid = tiles < num_sms() ? (int)tiles : num_sms();
+    return launch_kernel(kernel, grid, kMmThreads, C::kSmemBytes, s, nullptr, m.p, m.q, m.sp, m.sq,
+                         a);
+  } else {
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = PAIR ? 2u : (unsigned)a.split;
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    const long long grid = !PAIR ? tiles * a.split : 2 * (tiles < num_sms() / 2 ? tiles : num_sms() / 2);
+    return launch_kernel(kernel, (unsigned)grid, kMmThreads, C::kSmemBytes, s, &cluster, m.p, m.q,
+                         m.sp, m.sq, a);
+  }
+}
+
+// How a product is cut: the rows of a Q tile, pairs of CTAs (256 rows of P) or not, and how many
+// CTAs share a tile's depth.
+struct Plan {
+  int bn, pair, split;
+};
+
+// The cheapest cut by a model of the kernel's time: rounds of tiles over the SMs, a round being
+// the stages of a tile at the rate that the copies from L2 allow, and what a tile costs besides.
+// Measured on B200 (4096 x 4096, depths 256 to 16384; us a stage of 256 of the depth and us a tile
+// besides): pair 256 x 256 0.42 and 2.1, 128 x 192 0.57 and 1.1, 128 x 128 0.50 and 1.0, 128 x 64
+// 0.42 and 0.6; sharing a depth costs 2.2 more.
+// p, q: rows of P and Q, in `groups` ragged parts when given (tokens: p_ragged or not).
+Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_groups, int times,
+               int sms) {
+  const Plan cut[4] = {{256, 1, 1}, {192, 0, 1}, {128, 0, 1}, {64, 0, 1}};
+  const double stage_us[4] = {0.42, 0.57, 0.50, 0.42}, tile_us[4] = {2.1, 1.1, 1.0, 0.6};
+  Plan best = cut[0];
+  double best_us = 1e30;
+  const long long stages = (depth + kStageDepth - 1) / kStageDepth;
+  for (int i = 0; i < 4; ++i) {
+    const long long pr = cut[i].pair ? 256 : 128, bn = cut[i].bn;
+    // ragged: as if the groups had the same size
+    const long long pt = p_groups ? p_groups * ((p + p_groups * pr - 1) / (p_groups * pr)) : (p + pr - 1) / pr;
+    const long long qt = q_groups ? q_groups * ((q + q_groups * bn - 1) / (q_groups * bn)) : (q + bn - 1) / bn;
+    const long long tiles = pt * qt * times;
+    const long long units = cut[i].pair ? sms / 2 : sms;
+    for (int split = 1; split <= (bn <= 128 ? kMaxSplit : 1); ++split) {
+      if (split > 1 && (tiles * split > units || stages < 2 * split)) break;
+      const double us = (double)((tiles * split + units - 1) / units) *
+                        ((double)((stages + split - 1) / split) * stage_us[i] + tile_us[i] +
+                         (split > 1 ? 2.2 : 0.0));
+      if (us < best_us) {
+        best_us = us;
+        best = cut[i];
+        best.split = split;
+      }
+    }
+  }
+  return best;
+}
+
+template <int FMT, int BN, bool PAIR>
+cudaError_t launch_tiles(MmArgs a, const Maps& m, const Plan& p, cudaStream_t s) {
+  constexpr int PR = MmCfg<FMT, BN, PAIR>::kPRows;
+  a.pt = (a.p.rows + PR - 1) / PR;
+  a.qt = (a.q.rows + BN - 1) / BN;
+  // ragged rows: no more tiles than full ones and one partial for each group
+  const long long tiles = a.p.ragged   ? ((long long)a.p.rows / PR + a.groups) * a.qt
+                          : a.q.ragged ? ((long long)a.q.rows / BN + a.groups) * a.pt
+                          : (long long)a.pt * a.qt *
+                                (a.ragged == HINM_RAGGED_DEPTH ? a.groups : 1);
+  if (tiles > 0x3FFFFFFFll) return cudaErrorInvalidValue;
+  a.split = p.split;
+  if constexpr (BN <= 128 && !PAIR) {
+    if (p.split > 1) return run<FMT, BN, true, false>(a, m, tiles, s);
+  }
+  return run<FMT, BN, false, PAIR>(a, m, tiles, s);
 }
 
 template <int FMT>
-cudaError_t pick(const MmArgs& a, const hinm_fp4& A, const hinm_fp4& B, cudaStream_t s) {
+cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed,
+                 cudaStream_t s) {
+  const Fp4Geom ga = fp4_geom(A.rows, A.depth, A.ragged, A.groups);
+  const Fp4Geom gb = fp4_geom(B.rows, B.depth, B.ragged, B.groups);
+  const Side sa{A.scales, ga.row_tiles, ga.chunks(FMT), A.rows,
+                a.ragged == HINM_RAGGED_ROWS ? 1 : 0, 0};
+  const Side sb{B.scales, gb.row_tiles, gb.chunks(FMT), B.rows, 0,
+                a.ragged == HINM_RAGGED_ROWS ? 1 : 0};
+  a.steps = (int)(ga.depth_pad / 64);
   const int n = a.ragged == HINM_RAGGED_ROWS ? (B.rows + a.groups - 1) / a.groups : B.rows;
-  if (n <= 64) return run<FMT, 64>(a, A, B, s);
-  if (n <= 128) return run<FMT, 128>(a, A, B, s);
-  return run<FMT, 256>(a, A, B, s);
+  const bool swap = transposed && n > 64;  // tokens in the lanes
+  a.p = swap ? sb : sa;
+  a.q = swap ? sa : sb;
+  a.bias_q = swap;
+  a.q_major = transposed && !swap;
+  Maps m{};
+  if (!make_map(swap ? &m.q : &m.p, A.values, (long long)A.batch * A.rows, ga.pitch(), kBoxRows) ||
+      !make_map(swap ? &m.p : &m.q, B.values, B.rows, gb.pitch(), kBoxRows))
+    return cudaErrorInvalidValue;
+  const int g = a.ragged == HINM_RAGGED_ROWS ? a.groups : 0;
+  Plan p = make_plan(a.p.rows, a.q.rows,
+                     a.ragged == HINM_RAGGED_DEPTH ? a.depth / a.groups : a.depth,
+                     a.p.ragged ? g : 0, a.q.ragged ? g : 0,
+                     a.ragged == HINM_RAGGED_DEPTH ? a.groups : 1, num_sms());
+  if (p.pair) {
+    constexpr int kBox = kStageDepth / (4 * fp4_block(FMT));
+    if (!make_scale_map(swap ? &m.sq : &m.sp, A.scales, A.batch * ga.row_tiles * ga.chunks(FMT), kBox) ||
+        !make_scale_map(swap ? &m.sp : &m.sq, B.scales, gb.row_tiles * gb.chunks(FMT), kBox))
+      return cudaErrorInvalidValue;
+    return launch_tiles<FMT, 256, true>(a, m, p, s);
+  }
+  if (p.bn == 64) return launch_tiles<FMT, 64, false>(a, m, p, s);
+  if (p.bn == 128) return launch_tiles<FMT, 128, false>(a, m, p, s);
+  return launch_tiles<FMT, 192, false>(a, m, p, s);
 }
 
 }  // namespace
@@ -447,8 +1063,6 @@ cudaError_t pick(const MmArgs& a, const hinm_fp4& A, const hinm_fp4& B, cudaStre
 cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out& o, int* status,
                               cudaStream_t s) {
   MmArgs a{};
-  a.sa = A.scales;
-  a.sb = B.scales;
   a.ga = A.tensor_scale;
   a.gb = B.tensor_scale;
   a.bias = o.bias;
@@ -456,16 +1070,20 @@ cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out
   a.Y = o.Y;
   a.ldy = o.ldy;
   a.y_batch = o.batch_stride;
-  a.M = A.rows;
-  a.N = B.rows;
+  a.a_batched = A.batch > 1;
+  a.a_rows = A.rows;
   a.depth = B.depth;
   a.groups = B.groups;
   a.ragged = B.ragged;
   a.dtype = o.dtype;
-  a.transposed = o.transposed;
   a.act = o.act;
+  const long long es = o.dtype == HINM_DTYPE_F32 ? 4 : 2;
+  const unsigned long long bits =
+      reinterpret_cast<uintptr_t>(o.Y) | (uintptr_t)(o.ldy * es) | (uintptr_t)(o.batch_stride * es);
+  a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
   a.status = status;
-  return A.format == HINM_FP4_NV ? pick<HINM_FP4_NV>(a, A, B, s) : pick<HINM_FP4_MX>(a, A, B, s);
+  return A.format == HINM_FP4_NV ? pick<HINM_FP4_NV>(a, A, B, o.transposed != 0, s)
+                                 : pick<HINM_FP4_MX>(a, A, B, o.transposed != 0, s);
 }
 
 }  // namespace hinm

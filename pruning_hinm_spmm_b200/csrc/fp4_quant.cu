@@ -185,6 +185,7 @@ struct QArgs {
   const int32_t* offsets;
   int rows, depth, ragged, groups, vec;
   long long pitch, row_tiles, chunks, nblk;  // nblk: blocks of the stored depth
+  int early;  // let the stream's next kernel begin its set-up (few blocks)
   int* status;
 };
 
@@ -244,6 +245,7 @@ constexpr int kQWarps = 8;
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a) {
   ptx::enter_dependent();
+  if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
   using T = typename Elem<DT>::T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -300,6 +302,7 @@ constexpr int kQThreads = 128;
 template <int DT, int FMT, int V>
 __global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const QArgs a) {
   ptx::enter_dependent();
+  if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
   using T = typename Elem<DT>::T;
   const long long batch = blockIdx.z;
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const QArgs a) {
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs a) {
   ptx::enter_dependent();
+  if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
   using T = typename Elem<DT>::T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -427,6 +431,7 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
 template <int DT, int FMT, int V>
 __global__ void __launch_bounds__(kQThreads) dequant_cols_kernel(const QArgs a) {
   ptx::enter_dependent();
+  if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
   using T = typename Elem<DT>::T;
   const long long batch = blockIdx.z;
@@ -506,11 +511,13 @@ struct AmaxArgs {
   const int32_t* offsets;  // ragged: only positions in [offsets[0], offsets[groups]) count
   int rows, cols, groups, along_rows, vec;  // along_rows: the ragged dimension is the rows
   uint32_t* out;
+  int early;
 };
 
 template <int DT>
 __global__ void __launch_bounds__(256) amax_kernel(const AmaxArgs a) {
   ptx::enter_dependent();
+  if (a.early) ptx::launch_dependents();
   using T = typename Elem<DT>::T;
   constexpr int kRun = 16;
   const long long batch = blockIdx.y;
@@ -584,6 +591,9 @@ bool multiple(const void* p, long long ld, long long batch_stride, int batch, in
          (batch == 1 || (batch_stride * esize) % to == 0);
 }
 
+// Fewer blocks than would fill the SMs: the next kernel's set-up then fits beside them.
+bool few(dim3 grid) { return (long long)grid.x * grid.y * grid.z <= 148; }
+
 template <int DT, int FMT>
 cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
   constexpr int es = (int)sizeof(typename Elem<DT>::T);
@@ -592,6 +602,7 @@ cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
     a.vec = a.ragged != HINM_RAGGED_DEPTH && multiple(a.data, a.ld, a.batch_stride, batch, es, 16);
     const dim3 grid((unsigned)((a.rows + kFp4RowTile - 1) / kFp4RowTile * 4),
                     (unsigned)((a.nblk + 31) / 32), (unsigned)batch);
+    a.early = few(grid);
     return back ? launch_kernel(dequant_rows_kernel<DT, FMT>, grid, kQWarps * 32, 0, s, nullptr, a)
                 : launch_kernel(quant_rows_kernel<DT, FMT>, grid, kQWarps * 32, 0, s, nullptr, a);
   }
@@ -600,6 +611,7 @@ cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
   const int per = kQThreads * (two ? 2 : 1);
   const dim3 grid((unsigned)((a.rows + per - 1) / per),
                   (unsigned)(a.nblk * fp4_block(FMT) / kQDepth), (unsigned)batch);
+  a.early = few(grid);
   if (two)
     return back ? launch_kernel(dequant_cols_kernel<DT, FMT, 2>, grid, kQThreads, 0, s, nullptr, a)
                 : launch_kernel(quant_cols_kernel<DT, FMT, 2>, grid, kQThreads, 0, s, nullptr, a);
@@ -660,6 +672,7 @@ cudaError_t launch_fp4_tensor_scale(const void* src, int dtype, long long ld,
   if (blocks > 148 * 8) blocks = 148 * 8;
   if (blocks < 1) blocks = 1;
   const dim3 grid((unsigned)blocks, (unsigned)q.batch);
+  a.early = few(grid);
   switch (dtype) {
     case HINM_DTYPE_BF16:
       return launch_kernel(amax_kernel<HINM_DTYPE_BF16>, grid, 256, 0, s, nullptr, a);

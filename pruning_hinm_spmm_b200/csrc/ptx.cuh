@@ -49,6 +49,13 @@ __device__ __forceinline__ void enter_dependent() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets the stream's next kernel start its set-up once every block has called this (or ended);
+// its own wait still holds it until this kernel is complete.  Only where this kernel leaves
+// most of the SMs free.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- cp.async (16-, 8-, 4-byte)
 // dst: shared-memory address, src: global; both aligned to the size.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -63,6 +70,20 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // commits this thread's copies and waits for all of them
 __device__ __forceinline__ void cp_async_commit_wait_all() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- one thread of a warp
+// True in one lane of the (converged) warp, always the same one.  Unlike a test of the lane
+// number it tells the compiler that the guarded code runs once a warp, so that what it
+// computes from warp-uniform values stays in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 // ---------------------------------------------------------------- mbarrier
@@ -137,6 +158,10 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // 2-D tiled tensor load (box from the tensor map) at coordinates (x, y).
@@ -270,8 +295,84 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- tcgen05, pairs of CTAs
+// A cluster of two CTAs multiplies 256 rows (128 in each) by columns whose operand rows lie
+// half in each CTA; rank 0 issues, both hold their part of the accumulator.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void mma_fp4_block16_pair(uint32_t d_tmem, uint64_t a_desc,
+                                                     uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                                     uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_fp4_block32_pair(uint32_t d_tmem, uint64_t a_desc,
+                                                     uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                                     uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// In each CTA of the pair, from its own shared memory to its own tensor memory.
+__device__ __forceinline__ void tc_cp_32x128b_x4_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// tma_load_2d into this CTA, completing on a barrier of either CTA of the pair
+// (shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+// An arrival on the barrier of another CTA of the cluster, for tensor-memory reads that
+// tcgen05.wait and tcgen05.fence have ordered before it: relaxed, since a release at cluster
+// scope would also wait for every store to global memory that the thread has in flight (2000
+// cycles of a tile's time).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
 }
 
 // ---------------------------------------------------------------- descriptors
@@ -303,17 +404,17 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int n, int b_mn_major, i
   return d;
 }
 
-// Instruction descriptor, block-scaled e2m1: fp32 accumulator, both operands K-major, M = 128,
-// N = n.  e8m0: the scales' type (0: e4m3).  sf: which of the four scale bytes of a
+// Instruction descriptor, block-scaled e2m1: fp32 accumulator, both operands K-major, M = m (128,
+// or 256 for a pair of CTAs), N = n.  e8m0: the scales' type (0: e4m3).  sf: which of the four scale bytes of a
 // tensor-memory word the instruction starts at (both operands; 0 or 2).
-__host__ __device__ __forceinline__ uint32_t idesc_fp4(int n, int e8m0, int sf) {
+__host__ __device__ __forceinline__ uint32_t idesc_fp4(int m, int n, int e8m0, int sf) {
   uint32_t d = 0;
   d |= uint32_t(sf & 3) << 4;          // B scales' first byte
   d |= 1u << 7;                        // A format: e2m1
   d |= 1u << 10;                       // B format: e2m1
   d |= uint32_t((n >> 3) & 0x3F) << 17;
   d |= uint32_t(e8m0 & 1) << 23;       // scale type
-  d |= 1u << 27;                       // M = 128
+  d |= uint32_t((m >> 7) & 3) << 27;
   d |= uint32_t(sf & 3) << 29;         // A scales' first byte
   return d;
 }
@@ -334,6 +435,14 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
                "f"(c), "f"(d)
                : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
