@@ -47,7 +47,7 @@ namespace hinm {
 namespace {
 
 constexpr int kStageDepth = 256;  // of the depth in one stage: 128-byte rows
-constexpr int kBoxRows = 64;      // rows of one TMA box
+constexpr int kBoxRows = 64;      // rows of one TMA box: a tile loads as many as it has rows for
 
 // One side of the product.
 struct Side {
@@ -584,10 +584,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * C::kStageBytes);
             const int x = (int)(w.k0 / 2) + st * 128, q_row = w.q_row + rank * (mma_n(w.q_len) / 2);
             const int c = (int)c0 + st * C::kChunks;
-            for (int b = 0; b < 2; ++b) {
-              ptx::tma_load_2d_pair(P_s + b * kBoxRows * 128, &tmP, x, w.p_row + b * kBoxRows, bar);
-              ptx::tma_load_2d_pair(Q_s + b * kBoxRows * 128, &tmQ, x, q_row + b * kBoxRows, bar);
-            }
+            ptx::tma_load_2d_pair(P_s, &tmP, x, w.p_row, bar);
+            ptx::tma_load_2d_pair(Q_s, &tmQ, x, q_row, bar);
             ptx::tma_load_2d_pair(S_s, &tmSp, 0, (int)(w.p_tile * a.p.chunks) + c, bar);
             for (int j = 0; j < 2; ++j)
               ptx::tma_load_2d_pair(S_s + (1 + j) * C::kSfTile, &tmSq, 0,
@@ -935,7 +933,6 @@ int num_sms() {
   return n;
 }
 
-// box_rows is 64 for every map: a tile loads as many boxes as it has rows for.
 struct Maps {
   CUtensorMap p, q, sp, sq;  // values; scales (pairs)
 };
@@ -1037,15 +1034,18 @@ cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed
   a.q = swap ? sa : sb;
   a.bias_q = swap;
   a.q_major = transposed && !swap;
-  Maps m{};
-  if (!make_map(swap ? &m.q : &m.p, A.values, (long long)A.batch * A.rows, ga.pitch(), kBoxRows) ||
-      !make_map(swap ? &m.p : &m.q, B.values, B.rows, gb.pitch(), kBoxRows))
-    return cudaErrorInvalidValue;
   const int g = a.ragged == HINM_RAGGED_ROWS ? a.groups : 0;
   Plan p = make_plan(a.p.rows, a.q.rows,
                      a.ragged == HINM_RAGGED_DEPTH ? a.depth / a.groups : a.depth,
                      a.p.ragged ? g : 0, a.q.ragged ? g : 0,
                      a.ragged == HINM_RAGGED_DEPTH ? a.groups : 1, num_sms());
+  // a pair's boxes are what one CTA holds of a tile
+  Maps m{};
+  if (!make_map(swap ? &m.q : &m.p, A.values, (long long)A.batch * A.rows, ga.pitch(),
+                !p.pair ? kBoxRows : swap ? p.bn / 2 : 128) ||
+      !make_map(swap ? &m.p : &m.q, B.values, B.rows, gb.pitch(),
+                !p.pair ? kBoxRows : swap ? 128 : p.bn / 2))
+    return cudaErrorInvalidValue;
   if (p.pair) {
     constexpr int kBox = kStageDepth / (4 * fp4_block(FMT));
     if (!make_scale_map(swap ? &m.sq : &m.sp, A.scales, A.batch * ga.row_tiles * ga.chunks(FMT), kBox) ||

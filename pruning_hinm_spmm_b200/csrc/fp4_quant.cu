@@ -1,7 +1,7 @@
 // b1. Microscaled 4-bit quantisation (hinm.h, section b1): the tensor scale, the quantiser
 // and the way back.
 //
-//   NV: x' = fl32(x / g) (x times fl32(1/g)), s = e4m3(max |x'| / 6), code = e2m1(x' / s)
+//   NV: x' = fl32(x fl32(1/g)), s = e4m3(max |x'| / 6),               code = e2m1(x' / s)
 //   MX: s = 2^(floor(log2 max |x|) - 2),                              code = e2m1(x / s)
 //
 // Every rounding is to nearest, ties to even, decided on the exact quotient.  MX divides by
@@ -180,15 +180,15 @@ __device__ __forceinline__ BlockScale block_scale(const ScaleTable& t, uint32_t 
   }
   return b;
 }
-// The codes of 8 values (NV: over g).
+// The codes of 8 values x; NV: of 8 values -x, over g, so that the residual t s - x is one fused
+// operation and a zero keeps its sign (t = x r, q = t - (t s - x) r).
 template <int FMT>
 __device__ __forceinline__ uint32_t encode8(const F2 (&x)[4], const BlockScale& b) {
   float q[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    F2 t = mul2(x[i], F2(b.r, b.r));
-    if constexpr (FMT == HINM_FP4_NV)
-      t = fma2(fma2(t, F2(-b.s, -b.s), x[i]), F2(b.r, b.r), t);
+    F2 t = mul2(x[i], FMT == HINM_FP4_NV ? F2(-b.r, -b.r) : F2(b.r, b.r));
+    if constexpr (FMT == HINM_FP4_NV) t = fma2(fma2(t, F2(b.s, b.s), x[i]), F2(-b.r, -b.r), t);
     t.get(q[2 * i], q[2 * i + 1]);
   }
   return b.finite ? e2m1x8(q) : 0u;
@@ -201,7 +201,7 @@ __device__ __forceinline__ uint32_t encode_block(const ScaleTable& t, float (&v)
   uint32_t am = 0;
 #pragma unroll
   for (int i = 0; i < B; ++i) {
-    if constexpr (FMT == HINM_FP4_NV) v[i] = __fmul_rn(v[i], inv_g);
+    if constexpr (FMT == HINM_FP4_NV) v[i] = __fmul_rn(v[i], -inv_g);
     am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
   const BlockScale b = block_scale<FMT>(t, am);
@@ -233,7 +233,7 @@ __device__ __forceinline__ uint32_t encode_words(const uint32_t (&u)[4], float i
   F2 x[4] = {F2(l[0], h[0]), F2(l[1], h[1]), F2(l[2], h[2]), F2(l[3], h[3])};
   if constexpr (FMT == HINM_FP4_NV) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], F2(inv_g, inv_g));
+    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], F2(-inv_g, -inv_g));
   }
   return encode8<FMT>(x, b);
 }
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) 
         F2 x[4] = {F2(f[0], f[1]), F2(f[2], f[3]), F2(f[4], f[5]), F2(f[6], f[7])};
         if constexpr (FMT == HINM_FP4_NV) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], F2(inv_g, inv_g));
+          for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], F2(-inv_g, -inv_g));
         }
         w[h] = encode8<FMT>(x, b);
       }
