@@ -47,12 +47,11 @@ namespace hinm {
 namespace {
 
 constexpr int kStageDepth = 256;  // of the depth in one stage: 128-byte rows
-constexpr int kBoxRows = 64;      // rows of one TMA box: a tile loads as many as it has rows for
 
 // One side of the product.
 struct Side {
   const uint8_t* scales;
-  long long tiles, chunks;  // scale tiles of one matrix; chunks of a tile
+  int tiles, chunks;        // scale tiles of one matrix; chunks of a tile
   int rows;                 // of one matrix
   int batched;              // one matrix for each expert
   int ragged;               // its rows are the ragged tokens
@@ -89,6 +88,8 @@ struct MmCfg {
   static constexpr int kChunkDepth = 4 * fp4_block(FMT);
   static constexpr int kChunks = kStageDepth / kChunkDepth;  // scale chunks a stage
   static constexpr int kQTiles = BN > 128 ? 2 : 1;           // scale tiles of a Q tile
+  // rows of one copy of Q: a tile takes as many as it has rows for; few tokens cost few bytes
+  static constexpr int kQBox = PAIR ? BN / 2 : BN == 64 ? 16 : 64;
   static constexpr int kPBytes = 128 * 128;
   static constexpr int kPRows = PAIR ? 256 : 128;            // rows of a P tile
   static constexpr int kQBytes = (PAIR ? BN / 2 : BN) * 128; // a pair holds half of Q in each CTA
@@ -115,9 +116,9 @@ struct Tile {
   int p_row, q_row;            // first rows among all stored rows of P and Q
   int p_len, q_len;            // rows that count
   int p_out, q_out;            // their places in Y
-  long long p_tile, q_tile;    // scale tiles of the first rows
+  int p_tile, q_tile;          // scale tiles of the first rows
   int q_shift;                 // place of Q's first row in its scale tile (0 or 64)
-  long long k0;                // first stored depth
+  int k0;                      // first stored depth
   int steps;                   // products of 64
 };
 
@@ -126,9 +127,11 @@ struct Tile {
 template <int BN, int PR>
 __device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t, int pr) {
   Tile r;
+  r.e = 0;
   r.k0 = 0;
   r.steps = a.steps;
   int pi, qi;  // tile indexes of P and Q
+  int o = 0, end = 0;
   if (a.ragged == HINM_RAGGED_ROWS) {
     // tiles of one ragged tile stay together: its tokens are read once
     const int other = a.p.ragged ? a.qt : a.pt;
@@ -142,24 +145,27 @@ __device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t, 
     r.e = lo;
     pi = a.p.ragged ? u - cum[lo] : v;
     qi = a.p.ragged ? v : u - cum[lo];
+    o = __ldg(a.offsets + lo);
+    end = __ldg(a.offsets + lo + 1);
   } else {
-    const int per = a.pt * a.qt;
-    r.e = t / per;
-    t -= r.e * per;
-    pi = t % a.pt;
+    if (a.ragged == HINM_RAGGED_DEPTH) {
+      const int per = a.pt * a.qt;
+      r.e = t / per;
+      t -= r.e * per;
+      o = __ldg(a.offsets + r.e);
+      end = __ldg(a.offsets + r.e + 1);
+      r.k0 = (int)fp4_group_tile(o, r.e) * kFp4DepthPad;
+      r.steps = (end - o + kFp4DepthPad - 1) / kFp4DepthPad * 2;
+    }
     qi = t / a.pt;
-  }
-  int o = 0, end = 0;
-  if (a.ragged != HINM_RAGGED_NONE) {
-    o = __ldg(a.offsets + r.e);
-    end = __ldg(a.offsets + r.e + 1);
+    pi = t - qi * a.pt;
   }
   const int p = pi * PR + pr * 128, q = qi * BN;
   r.q_shift = q % kFp4RowTile;
   if (a.p.ragged) {
     r.p_row = r.p_out = o + p;
     r.p_len = min(128, end - r.p_row);
-    r.p_tile = fp4_group_tile(o, r.e) + p / 128;
+    r.p_tile = (int)fp4_group_tile(o, r.e) + p / 128;
   } else {
     const int m = a.p.batched ? r.e : 0;
     r.p_row = m * a.p.rows + p;
@@ -170,17 +176,13 @@ __device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t, 
   if (a.q.ragged) {
     r.q_row = r.q_out = o + q;
     r.q_len = min(BN, end - r.q_row);
-    r.q_tile = fp4_group_tile(o, r.e) + q / kFp4RowTile;
+    r.q_tile = (int)fp4_group_tile(o, r.e) + q / kFp4RowTile;
   } else {
     const int m = a.q.batched ? r.e : 0;
     r.q_row = m * a.q.rows + q;
     r.q_out = q;
     r.q_len = min(BN, a.q.rows - q);
     r.q_tile = m * a.q.tiles + q / kFp4RowTile;
-  }
-  if (a.ragged == HINM_RAGGED_DEPTH) {
-    r.k0 = fp4_group_tile(o, r.e) * kFp4DepthPad;
-    r.steps = (end - o + kFp4DepthPad - 1) / kFp4DepthPad * 2;
   }
   return r;
 }
@@ -559,12 +561,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       bool stop = false;
       for (int t = first; t < tiles && !stop; t += step) {
         const Tile w = tile_at(t);
-        const long long c0 = w.k0 / C::kChunkDepth;
-        const uint8_t* sp = a.p.scales + (w.p_tile * a.p.chunks + c0) * kFp4ChunkBytes;
-        const uint8_t* sq = a.q.scales + (w.q_tile * a.q.chunks + c0) * kFp4ChunkBytes;
+        const int c0 = w.k0 / C::kChunkDepth;
+        const uint8_t* sp =
+            a.p.scales + ((long long)w.p_tile * a.p.chunks + c0) * kFp4ChunkBytes;
+        const uint8_t* sq =
+            a.q.scales + ((long long)w.q_tile * a.q.chunks + c0) * kFp4ChunkBytes;
         const bool two = C::kQTiles == 2 && w.q_shift + w.q_len > kFp4RowTile;
-        const int pb = (w.p_len + kBoxRows - 1) / kBoxRows;
-        const int qb = (w.q_len + kBoxRows - 1) / kBoxRows;
+        const int qb = (w.q_len + C::kQBox - 1) / C::kQBox;
         int s0, s1;
         stage_range(w.steps, s0, s1);
         for (int st = s0; st < s1; ++st, ++it) {
@@ -582,28 +585,27 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             // completing on rank 0's barrier; scales as boxes of the stage's chunks
             const uint32_t bar = ptx::mapa_shared(full_bar(s), 0);
             if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * C::kStageBytes);
-            const int x = (int)(w.k0 / 2) + st * 128, q_row = w.q_row + rank * (mma_n(w.q_len) / 2);
-            const int c = (int)c0 + st * C::kChunks;
+            const int x = w.k0 / 2 + st * 128, q_row = w.q_row + rank * (mma_n(w.q_len) / 2);
+            const int c = c0 + st * C::kChunks;
             ptx::tma_load_2d_pair(P_s, &tmP, x, w.p_row, bar);
             ptx::tma_load_2d_pair(Q_s, &tmQ, x, q_row, bar);
-            ptx::tma_load_2d_pair(S_s, &tmSp, 0, (int)(w.p_tile * a.p.chunks) + c, bar);
+            ptx::tma_load_2d_pair(S_s, &tmSp, 0, w.p_tile * a.p.chunks + c, bar);
             for (int j = 0; j < 2; ++j)
               ptx::tma_load_2d_pair(S_s + (1 + j) * C::kSfTile, &tmSq, 0,
-                                    (int)((w.q_tile + j) * a.q.chunks) + c, bar);
+                                    (w.q_tile + j) * a.q.chunks + c, bar);
             continue;
           }
-          ptx::mbar_arrive_expect_tx(full_bar(s), (uint32_t)(pb + qb) * (kBoxRows * 128) +
+          ptx::mbar_arrive_expect_tx(full_bar(s), C::kPBytes + (uint32_t)qb * (C::kQBox * 128) +
                                                       sf * (two ? 3 : 2));
-          const int x = (int)(w.k0 / 2) + st * 128;
-          for (int b = 0; b < pb; ++b)
-            ptx::tma_load_2d(P_s + b * kBoxRows * 128, &tmP, x, w.p_row + b * kBoxRows, full_bar(s));
+          const int x = w.k0 / 2 + st * 128;
+          ptx::tma_load_2d(P_s, &tmP, x, w.p_row, full_bar(s));
           for (int b = 0; b < qb; ++b)
-            ptx::tma_load_2d(Q_s + b * kBoxRows * 128, &tmQ, x, w.q_row + b * kBoxRows, full_bar(s));
+            ptx::tma_load_2d(Q_s + b * C::kQBox * 128, &tmQ, x, w.q_row + b * C::kQBox, full_bar(s));
           const long long at = (long long)st * C::kSfTile;
           ptx::bulk_g2s(S_s, sp + at, sf, full_bar(s));
           ptx::bulk_g2s(S_s + C::kSfTile, sq + at, sf, full_bar(s));
           if (two)
-            ptx::bulk_g2s(S_s + 2 * C::kSfTile, sq + a.q.chunks * kFp4ChunkBytes + at, sf,
+            ptx::bulk_g2s(S_s + 2 * C::kSfTile, sq + (long long)a.q.chunks * kFp4ChunkBytes + at, sf,
                           full_bar(s));
         }
       }
@@ -719,10 +721,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     for (int t = first; t < tiles; t += step, ++lu) {
       const Tile w = tile_at(t);
       const int b = (int)(lu % C::kAccBufs);
-      bool ok = true;  // one lane asks, so that the waiting warps take few issue slots
-      if (lane == 0) ok = ptx::mbar_wait(accf_bar(b), (lu / C::kAccBufs) & 1, a.status, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      ptx::tc_fence_after();
+      // (loaded while the products run)
       int s0, s1;
       stage_range(w.steps, s0, s1);
       const int m = a.a_batched ? w.e : 0;
@@ -730,6 +729,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       const float* bias = a.bias ? a.bias + (long long)m * a.a_rows : nullptr;
       const bool mine = row < w.p_len;
       const float bias_p = bias && !a.bias_q && mine ? __ldg(bias + w.p_out + row) : 0.0f;
+      bool ok = true;  // one lane asks, so that the waiting warps take few issue slots
+      if (lane == 0) ok = ptx::mbar_wait(accf_bar(b), (lu / C::kAccBufs) & 1, a.status, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      ptx::tc_fence_after();
       const long long y0 = a.ragged == HINM_RAGGED_DEPTH ? w.e * a.y_batch : 0;
       const int col0 = part * kOwn, col1 = min(w.q_len, col0 + kOwn);
       const uint32_t tile = ptx::smem_u32(epi_smem + (warp - 2) * kEpiTile);
@@ -1023,9 +1026,11 @@ cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed
                  cudaStream_t s) {
   const Fp4Geom ga = fp4_geom(A.rows, A.depth, A.ragged, A.groups);
   const Fp4Geom gb = fp4_geom(B.rows, B.depth, B.ragged, B.groups);
-  const Side sa{A.scales, ga.row_tiles, ga.chunks(FMT), A.rows,
+  if (A.batch * ga.row_tiles * ga.chunks(FMT) > 0x7FFFFFFF || gb.row_tiles * gb.chunks(FMT) > 0x7FFFFFFF)
+    return cudaErrorInvalidValue;
+  const Side sa{A.scales, (int)ga.row_tiles, (int)ga.chunks(FMT), A.rows,
                 a.ragged == HINM_RAGGED_ROWS ? 1 : 0, 0};
-  const Side sb{B.scales, gb.row_tiles, gb.chunks(FMT), B.rows, 0,
+  const Side sb{B.scales, (int)gb.row_tiles, (int)gb.chunks(FMT), B.rows, 0,
                 a.ragged == HINM_RAGGED_ROWS ? 1 : 0};
   a.steps = (int)(ga.depth_pad / 64);
   const int n = a.ragged == HINM_RAGGED_ROWS ? (B.rows + a.groups - 1) / a.groups : B.rows;
@@ -1039,12 +1044,11 @@ cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed
                      a.ragged == HINM_RAGGED_DEPTH ? a.depth / a.groups : a.depth,
                      a.p.ragged ? g : 0, a.q.ragged ? g : 0,
                      a.ragged == HINM_RAGGED_DEPTH ? a.groups : 1, num_sms());
-  // a pair's boxes are what one CTA holds of a tile
   Maps m{};
+  const int q_box = p.pair ? p.bn / 2 : p.bn == 64 ? 16 : 64;  // MmCfg::kQBox
   if (!make_map(swap ? &m.q : &m.p, A.values, (long long)A.batch * A.rows, ga.pitch(),
-                !p.pair ? kBoxRows : swap ? p.bn / 2 : 128) ||
-      !make_map(swap ? &m.p : &m.q, B.values, B.rows, gb.pitch(),
-                !p.pair ? kBoxRows : swap ? 128 : p.bn / 2))
+                swap ? q_box : 128) ||
+      !make_map(swap ? &m.p : &m.q, B.values, B.rows, gb.pitch(), swap ? 128 : q_box))
     return cudaErrorInvalidValue;
   if (p.pair) {
     constexpr int kBox = kStageDepth / (4 * fp4_block(FMT));

@@ -307,15 +307,10 @@ struct QArgs {
   int* status;
 };
 
-// Where a stored row's scales lie: its tile and its place in it.  false: the row is in no group.
-__device__ __forceinline__ bool row_place(const QArgs& a, int row, long long& tile, int& at) {
-  if (a.ragged != HINM_RAGGED_ROWS) {
-    tile = row / kFp4RowTile;
-    at = row % kFp4RowTile;
-    return true;
-  }
-  // the last of several groups that start at one row is the one that may hold it
-  const int e = group_of(a.groups, row, [&](int i) { return (long long)__ldg(a.offsets + i); });
+// Where the scales of a row of ragged group e (-1: before the first) lie: its tile and its place in
+// it.  false: the row is in no group.
+__device__ __forceinline__ bool place_in(const QArgs& a, int row, int e, long long& tile, int& at) {
+  if (e < 0) return false;
   const int o = __ldg(a.offsets + e), end = __ldg(a.offsets + e + 1);
   if (row < o || row >= end) return false;
   tile = fp4_group_tile(o, e) + (row - o) / kFp4RowTile;
@@ -327,6 +322,33 @@ __device__ __forceinline__ bool row_place(const QArgs& a, int row, long long& ti
   return true;
 }
 
+// The same for any stored row, its group looked for.
+__device__ __forceinline__ bool row_place(const QArgs& a, int row, long long& tile, int& at) {
+  if (a.ragged != HINM_RAGGED_ROWS) {
+    tile = row / kFp4RowTile;
+    at = row % kFp4RowTile;
+    return true;
+  }
+  // the last of several groups that start at one row is the one that may hold it
+  return place_in(a, row,
+                  group_of(a.groups, row, [&](int i) { return (long long)__ldg(a.offsets + i); }),
+                  tile, at);
+}
+
+// The last of the groups that start at or before each of N rows of a warp (the same rows in every
+// lane; row_place finds one row's with a chain of loads, this takes 32 groups a load).
+template <int N>
+__device__ __forceinline__ void groups_of_rows(const QArgs& a, int row0, int step, int (&e)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = -1;
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < a.groups; base += 32) {
+    const int i = base + lane;
+    const int o = i < a.groups ? __ldg(a.offsets + i) : 0x7FFFFFFF;
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] += __popc(__ballot_sync(0xFFFFFFFFu, o <= row0 + step * j));
+  }
+}
 // Where the stored depth p (a multiple of a block) comes from: the first source position and
 // how many of the `count` positions are real.  false: p is in no group's stored range.
 __device__ __forceinline__ bool depth_place(const QArgs& a, long long p, int count, int& src,
@@ -374,12 +396,15 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* u) {
                : "memory");
 }
 
-// Keeps the elements of 16-bit pairs whose bits are set (two bits a word).
+// Keeps the elements of a 16-bit pair whose bits (0 and 1) are set: each bit moved to a byte's sign,
+// which the permutation copies over the element's bits.
 __device__ __forceinline__ uint32_t masked(uint32_t u, uint32_t bits2) {
-  return u & ((bits2 & 1u ? 0xFFFFu : 0u) | (bits2 & 2u ? 0xFFFF0000u : 0u));
+  uint32_t m;
+  asm("prmt.b32 %0, %1, %2, 0xCC88;" : "=r"(m) : "r"(bits2 << 7), "r"(bits2 << 6));
+  return u & m;
 }
 
-template <int DT, int FMT, bool VEC>
+template <int DT, int FMT, bool VEC, bool RAGGED>
 __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a) {
   __shared__ ScaleTable table;
   fill<FMT>(table);
@@ -398,18 +423,31 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
   int k = 0, real = 0;
   const bool mine = blk < a.nblk && depth_place(a, blk * B, B, k, real);
   const bool chunk_ok = __shfl_sync(0xFFFFFFFFu, mine, lane & ~3);
+  long long tile[4];
+  int at[4];
+  bool placed[4] = {true, true, true, true};
+  if constexpr (RAGGED) {
+    int e[4];
+    groups_of_rows<4>(a, row0, 32, e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      placed[j] = row0 + 32 * j < a.rows && place_in(a, row0 + 32 * j, e[j], tile[j], at[j]);
+  }
   // (blocks of 32 fp32 values: two rows at once, to stay in registers)
   constexpr int kAtOnce = kWords > 16 ? 2 : 4;
   uint32_t word[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j0 = 0; j0 < 4; j0 += kAtOnce) {
-    uint32_t u[kAtOnce][kWords];
+    uint32_t u[kAtOnce][kWords], keep[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       const int row = row0 + 32 * (j0 + j);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) u[j][i] = 0;
-      if (row >= a.rows || real <= 0) continue;
+      keep[j] = 0xFFFFFFFFu;
+      if (row >= a.rows || real <= 0 || !placed[j0 + j]) continue;
+      if (a.bits)
+        keep[j] = __ldg(a.bits + (batch * a.rows + row) * ((a.depth + 31) / 32) + k / 32) >> (k % 32);
       const T* p = src + (long long)row * a.ld + k;
       if (VEC && real == B) {
         if (a.vec == 32) {
@@ -434,15 +472,6 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
           }
         }
       }
-      if (a.bits) {
-        const long long words = (a.depth + 31) / 32;
-        const uint32_t m = __ldg(a.bits + (batch * a.rows + row) * words + k / 32) >> (k % 32);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          if constexpr (k16) u[j][i] = masked(u[j][i], m >> (2 * i));
-          else u[j][i] = (m >> i) & 1u ? u[j][i] : 0u;
-        }
-      }
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
@@ -451,6 +480,13 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
       uint32_t code = 0;
       if (mine) {
         uint32_t w[B / 8];
+        if (a.bits) {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            if constexpr (k16) u[j][i] = masked(u[j][i], keep[j] >> (2 * i));
+            else u[j][i] = (keep[j] >> i) & 1u ? u[j][i] : 0u;
+          }
+        }
         if constexpr (k16) {
           uint32_t m = 0;
 #pragma unroll
@@ -466,10 +502,7 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
           for (int i = 0; i < B; ++i) v[i] = __uint_as_float(u[j][i]);
           code = encode_block<FMT, B>(table, v, inv_g, w);
         }
-        // a row of no group keeps what it holds
-        long long tile;
-        int at;
-        if (a.ragged != HINM_RAGGED_ROWS || row_place(a, row, tile, at)) {
+        if (placed[j0 + j]) {  // a row of no group keeps what it holds
           uint8_t* out = a.values + (batch * a.rows + row) * a.pitch + blk * (B / 2);
           if constexpr (FMT == HINM_FP4_NV) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
           else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -483,7 +516,7 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
   }
   if ((lane & 3) != 0 || !chunk_ok) return;
   const long long chunk = blk / 4;
-  if (a.ragged != HINM_RAGGED_ROWS) {
+  if constexpr (!RAGGED) {
     if (row0 >= a.rows) return;
     uint32_t* s = reinterpret_cast<uint32_t*>(
         a.scales + ((batch * a.row_tiles + row0 / kFp4RowTile) * a.chunks + chunk) * kFp4ChunkBytes +
@@ -498,12 +531,9 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = row0 + 32 * j;
-      long long tile;
-      int at;
-      if (row < a.rows && row_place(a, row, tile, at))
-        *reinterpret_cast<uint32_t*>(a.scales + (tile * a.chunks + chunk) * kFp4ChunkBytes +
-                                     (at % 32) * 16 + (at / 32) * 4) = word[j];
+      if (placed[j])
+        *reinterpret_cast<uint32_t*>(a.scales + (tile[j] * a.chunks + chunk) * kFp4ChunkBytes +
+                                     (at[j] % 32) * 16 + (at[j] / 32) * 4) = word[j];
     }
   }
 }
@@ -927,6 +957,16 @@ __device__ __forceinline__ uint32_t widest16(uint32_t m, const uint4& t) {
   }
   return m;
 }
+// The elements of 16 bytes whose bits are set.
+template <int DT>
+__device__ __forceinline__ uint4 masked_piece(const uint4& t, uint32_t k) {
+  if constexpr (DT == HINM_DTYPE_F32)
+    return make_uint4(k & 1u ? t.x : 0u, k & 2u ? t.y : 0u, k & 4u ? t.z : 0u, k & 8u ? t.w : 0u);
+  else
+    return make_uint4(masked(t.x, k), masked(t.y, k >> 2), masked(t.z, k >> 4), masked(t.w, k >> 6));
+}
+constexpr int kAhead = 4;  // pieces of 16 bytes that a thread loads before it uses the first
+
 template <int DT>
 __device__ __forceinline__ uint32_t infinite(uint32_t m) {  // some magnitude is not finite
   if constexpr (DT == HINM_DTYPE_F32) return m >= 0x7F800000u;
@@ -944,23 +984,34 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
   const T* src = reinterpret_cast<const T*>(a.src) + batch * a.batch_stride;
   const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long threads = (long long)gridDim.x * blockDim.x;
+  const long long words = (a.cols + 31) / 32;
   uint32_t m = 0;
-  if (a.vec && !a.bits && a.ld == a.cols && c0 == 0 && c1 == a.cols) {
+  if (a.vec && a.ld == a.cols && c0 == 0 && c1 == a.cols && (!a.bits || a.cols % 32 == 0)) {
     const uint4* p = reinterpret_cast<const uint4*>(src + (long long)r0 * a.cols);
     const long long n = (long long)(r1 - r0) * a.cols / kPer;
-    long long i = tid;
-    for (; i + 3 * threads < n; i += 4 * threads) {
-      uint4 t[4];
+    // whole words of mask a row: the bits run along with the elements, kPer of them a piece
+    const uint8_t* bits =
+        a.bits ? reinterpret_cast<const uint8_t*>(a.bits + (batch * a.rows + r0) * words) : nullptr;
+    for (long long i = tid; i < n; i += kAhead * threads) {
+      uint4 t[kAhead];
+      uint32_t k[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = __ldg(p + i + j * threads);
+      for (int j = 0; j < kAhead; ++j) {
+        const long long at = i + j * threads;
+        t[j] = make_uint4(0, 0, 0, 0);
+        k[j] = 0;
+        if (at < n) {
+          t[j] = __ldg(p + at);
+          if (bits) k[j] = kPer == 8 ? __ldg(bits + at) : __ldg(bits + at / 2) >> (4 * (at & 1));
+        }
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = widest16<DT, FINITE>(m, t[j]);
+      for (int j = 0; j < kAhead; ++j)
+        m = widest16<DT, FINITE>(m, bits ? masked_piece<DT>(t[j], k[j]) : t[j]);
     }
-    for (; i < n; i += threads) m = widest16<DT, FINITE>(m, __ldg(p + i));
     return m;
   }
   // warps along the rows, lanes along a row's pieces (elements where they are not aligned)
-  const long long words = (a.cols + 31) / 32;
   const int lane = threadIdx.x & 31;
   for (long long row = r0 + (tid >> 5); row < r1; row += threads >> 5) {
     const T* p = src + row * a.ld;
@@ -968,16 +1019,7 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
     if (a.vec && c0 == 0 && c1 == a.cols) {
       for (int c = lane * kPer; c < a.cols; c += 32 * kPer) {
         uint4 t = __ldg(reinterpret_cast<const uint4*>(p + c));
-        if (bits) {
-          const uint32_t k = __ldg(bits + c / 32) >> (c % 32);
-          if constexpr (sizeof(T) == 2) {
-            t = make_uint4(masked(t.x, k), masked(t.y, k >> 2), masked(t.z, k >> 4),
-                           masked(t.w, k >> 6));
-          } else {
-            t = make_uint4(k & 1u ? t.x : 0u, k & 2u ? t.y : 0u, k & 4u ? t.z : 0u,
-                           k & 8u ? t.w : 0u);
-          }
-        }
+        if (bits) t = masked_piece<DT>(t, __ldg(bits + c / 32) >> (c % 32));
         m = widest16<DT, FINITE>(m, t);
       }
     } else {
@@ -988,6 +1030,14 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
     }
   }
   return m;
+}
+
+// (A kernel and not a memset, so that the next kernel's launch overlaps it.)
+__global__ void __launch_bounds__(256) zero_kernel(uint32_t* out, int n) {
+  ptx::enter_dependent();
+  ptx::launch_dependents();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) out[i] = 0;
 }
 
 template <int DT>
@@ -1069,10 +1119,12 @@ cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
     a.early = few(grid);
     if (back)
       return launch_kernel(dequant_rows_kernel<DT, FMT>, grid, kQWarps * 32, 0, s, nullptr, a);
-    return a.vec
-               ? launch_kernel(quant_rows_kernel<DT, FMT, true>, grid, kQWarps * 32, 0, s, nullptr, a)
-               : launch_kernel(quant_rows_kernel<DT, FMT, false>, grid, kQWarps * 32, 0, s, nullptr,
-                               a);
+    auto kernel = a.ragged == HINM_RAGGED_ROWS
+                      ? (a.vec ? quant_rows_kernel<DT, FMT, true, true>
+                               : quant_rows_kernel<DT, FMT, false, true>)
+                      : (a.vec ? quant_rows_kernel<DT, FMT, true, false>
+                               : quant_rows_kernel<DT, FMT, false, false>);
+    return launch_kernel(kernel, grid, kQWarps * 32, 0, s, nullptr, a);
   }
   const unsigned ny = (unsigned)(a.nblk * fp4_block(FMT) / kQDepth);
   constexpr int kCols = 16 / es;
@@ -1141,14 +1193,15 @@ cudaError_t launch_fp4_tensor_scale(const void* src, int dtype, long long ld,
   a.out = reinterpret_cast<uint32_t*>(q.tensor_scale);
   const int es = dtype == HINM_DTYPE_F32 ? 4 : 2;
   a.vec = a.cols * es % 16 == 0 && multiple(src, ld, batch_stride, q.batch, es, 16);
-  // 4 pieces of 16 bytes a thread and up; one block a matrix needs no other's maximum and no
-  // starting value
+  // kAhead pieces of 16 bytes a thread; one block a matrix (of up to 64 KB) needs no other's maximum
+  // and no starting value
   const long long pieces = (long long)a.rows * a.cols * es / 16;
-  long long blocks = (pieces + 256 * 4 - 1) / (256 * 4);
+  long long blocks = (pieces + 256 * kAhead - 1) / (256 * kAhead);
   if (blocks * q.batch > 148 * 8) blocks = (148 * 8 + q.batch - 1) / q.batch;
   a.one = blocks <= 4;
   if (a.one) blocks = 1;
-  else if (cudaError_t e = cudaMemsetAsync(q.tensor_scale, 0, (size_t)q.batch * 4, s);
+  else if (cudaError_t e = launch_kernel(zero_kernel, dim3((unsigned)((q.batch + 255) / 256)), 256, 0,
+                                         s, nullptr, a.out, q.batch);
            e != cudaSuccess)
     return e;
   const dim3 grid((unsigned)blocks, (unsigned)q.batch);
