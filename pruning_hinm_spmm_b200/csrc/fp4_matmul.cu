@@ -319,19 +319,28 @@ __device__ __forceinline__ void write_tile(const MmArgs& a, uint32_t tile, int l
         *reinterpret_cast<uint4*>(y0 + r * pitch + p * 16) = ptx::ld_shared_v4(piece(tile, r, p));
     }
   } else {
-    // rows that start anywhere: element by element, lanes along a row
-#pragma unroll 4
-    for (int r = 0; r < min(rows, 32); ++r) {
-      for (int c = lane; c < n; c += 32) {
-        const uint32_t from = piece(tile, r, c * es / 16) + c * es % 16;
-        if (es == 4) {
-          uint32_t v;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
-          *reinterpret_cast<uint32_t*>(y0 + r * pitch + c * 4) = v;
-        } else {
-          uint16_t v;
-          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from) : "memory");
-          *reinterpret_cast<uint16_t*>(y0 + r * pitch + c * 2) = v;
+    // rows that start anywhere: element by element, lanes along a row, 8 rows at a time
+    for (int c = lane; c < n; c += 32) {
+#pragma unroll 1
+      for (int r0 = 0; r0 < min(rows, 32); r0 += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t from = piece(tile, r0 + i, c * es / 16) + c * es % 16;
+          if (es == 4) {
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[i]) : "r"(from) : "memory");
+          } else {
+            uint16_t h;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(from) : "memory");
+            v[i] = h;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (r0 + i >= rows) continue;
+          char* to = y0 + (r0 + i) * pitch + c * es;
+          if (es == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
+          else *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
         }
       }
     }
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             ptx::tma_load_2d_pair(P_s, &tmP, x, w.p_row, bar);
             ptx::tma_load_2d_pair(Q_s, &tmQ, x, q_row, bar);
             ptx::tma_load_2d_pair(S_s, &tmSp, 0, w.p_tile * a.p.chunks + c, bar);
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < C::kQTiles; ++j)
               ptx::tma_load_2d_pair(S_s + (1 + j) * C::kSfTile, &tmSq, 0,
                                     (w.q_tile + j) * a.q.chunks + c, bar);
             continue;
@@ -971,13 +980,16 @@ struct Plan {
 // The cheapest cut by a model of the kernel's time: rounds of tiles over the SMs, a round being
 // the stages of a tile at the rate that the copies from L2 allow, and what a tile costs besides.
 // Measured on B200 (4096 x 4096, depths 256 to 16384; us a stage of 256 of the depth and us a tile
-// besides): pair 256 x 256 0.42 and 2.1, 128 x 192 0.57 and 1.1, 128 x 128 0.50 and 1.0, 128 x 64
-// 0.42 and 0.6; sharing a depth costs 2.2 more.
+// besides): pair 256 x 256 0.40 and 2.1, 128 x 192 0.465 and 0.95, 128 x 128 0.42 and 0.7, 128 x 64
+// 0.45 and 0.6; the last tile's columns are written after everything else, 0.011 a column.  So at depth 1024 128 x 192 takes 17.0 us and pairs 17.7, at 4096 45.0 and 35.9, at
+// 16384 156 and 115.  Sharing a tile's depth costs 1.5 us and 0.03 a column (partial sums through
+// the cluster): 4096 rows of depth 4096 by 1 column 7.1 us shared by four and 9.5 not, by 256
+// columns 13.1 shared by two and 10.4 not.
 // p, q: rows of P and Q, in `groups` ragged parts when given (tokens: p_ragged or not).
 Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_groups, int times,
                int sms) {
   const Plan cut[4] = {{256, 1, 1}, {192, 0, 1}, {128, 0, 1}, {64, 0, 1}};
-  const double stage_us[4] = {0.42, 0.57, 0.50, 0.42}, tile_us[4] = {2.1, 1.1, 1.0, 0.6};
+  const double stage_us[4] = {0.40, 0.465, 0.42, 0.45}, tile_us[4] = {2.1, 0.95, 0.7, 0.6};
   Plan best = cut[0];
   double best_us = 1e30;
   const long long stages = (depth + kStageDepth - 1) / kStageDepth;
@@ -992,7 +1004,8 @@ Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_gr
       if (split > 1 && (tiles * split > units || stages < 2 * split)) break;
       const double us = (double)((tiles * split + units - 1) / units) *
                         ((double)((stages + split - 1) / split) * stage_us[i] + tile_us[i] +
-                         (split > 1 ? 2.2 : 0.0));
+                         (split > 1 ? 1.5 + 0.03 * (double)(q < bn ? q : bn) : 0.0)) +
+                        0.011 * (double)bn;
       if (us < best_us) {
         best_us = us;
         best = cut[i];
