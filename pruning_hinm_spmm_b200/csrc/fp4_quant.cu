@@ -415,10 +415,13 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
   constexpr bool k16 = sizeof(T) == 2;
   constexpr int kWords = B * (int)sizeof(T) / 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kRead = kWords + (VEC ? 0 : 4);  // words read of a block
   const long long batch = blockIdx.z;
   const long long blk = (long long)blockIdx.y * 32 + lane;
   const int row0 = ((int)blockIdx.x >> 2) * kFp4RowTile + ((int)blockIdx.x & 3) * kQWarps + warp;
   const T* src = reinterpret_cast<const T*>(a.data) + batch * a.batch_stride;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(src);
+  const uintptr_t hi = lo + ((unsigned long long)(a.rows - 1) * a.ld + a.depth) * sizeof(T);
   const float inv_g = FMT == HINM_FP4_NV && a.g ? __frcp_rn(__ldg(a.g + batch)) : 1.0f;
   int k = 0, real = 0;
   const bool mine = blk < a.nblk && depth_place(a, blk * B, B, k, real);
@@ -438,17 +441,23 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
   uint32_t word[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j0 = 0; j0 < 4; j0 += kAtOnce) {
-    uint32_t u[kAtOnce][kWords], keep[kAtOnce];
+    uint32_t u[kAtOnce][kRead], keep[kAtOnce];
+    int shift[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       const int row = row0 + 32 * (j0 + j);
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) u[j][i] = 0;
+      for (int i = 0; i < kRead; ++i) u[j][i] = 0;
+      shift[j] = 0;
       keep[j] = 0xFFFFFFFFu;
       if (row >= a.rows || real <= 0 || !placed[j0 + j]) continue;
+      const T* p = src + (long long)row * a.ld;
       if (a.bits)
         keep[j] = __ldg(a.bits + (batch * a.rows + row) * ((a.depth + 31) / 32) + k / 32) >> (k % 32);
-      const T* p = src + (long long)row * a.ld + k;
+      p += k;
+      // (rows that are not aligned: the aligned 16-byte pieces around the block, unless they reach
+      // out of the matrix)
+      const uintptr_t at0 = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
       if (VEC && real == B) {
         if (a.vec == 32) {
 #pragma unroll
@@ -463,6 +472,16 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
             u[j][i + 3] = t.w;
           }
         }
+      } else if (!VEC && real == B && at0 >= lo && at0 + 4 * kRead <= hi) {
+        shift[j] = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+#pragma unroll
+        for (int i = 0; i < kRead; i += 4) {
+          const uint4 t = __ldg(reinterpret_cast<const uint4*>(at0) + i / 4);
+          u[j][i] = t.x;
+          u[j][i + 1] = t.y;
+          u[j][i + 2] = t.z;
+          u[j][i + 3] = t.w;
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < B; ++i) {
@@ -470,6 +489,23 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
             if constexpr (k16) u[j][i / 2] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
             else u[j][i] = __ldg(p + i);
           }
+        }
+      }
+    }
+    if constexpr (!VEC) {  // the block's words out of what was read
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (shift[j] & 8) {
+#pragma unroll
+          for (int i = 0; i + 2 < kRead; ++i) u[j][i] = u[j][i + 2];
+        }
+        if (shift[j] & 4) {
+#pragma unroll
+          for (int i = 0; i + 1 < kRead; ++i) u[j][i] = u[j][i + 1];
+        }
+        if (k16 && (shift[j] & 2)) {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) u[j][i] = __funnelshift_r(u[j][i], u[j][i + 1], 16);
         }
       }
     }
@@ -727,20 +763,42 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) 
 // ------------------------------------------------------------------ back
 // value = fl32(code s g): code * s has at most 6 significant bits, so the only rounding in
 // fp32 is that of the product with g (none when g is a power of two).
-template <int DT, int FMT>
+// Rows that are not aligned, in a warp's own shared memory: lane l's block of n elements starts at
+// l * kPitch (16 bytes more than the block, so that lanes do not meet in a bank), and 32 consecutive
+// elements go to memory at a time.  (A lane's block element by element touches 32 lines at a time:
+// 4883 x 3382 bf16 NV took 112 us, this way 21.)
+template <class T, int B>
+struct Staged {
+  static constexpr int kPitch = B * (int)sizeof(T) + 16;
+  static constexpr int kBytes = 32 * kPitch;
+  // Element i of the warp's 32 B, its place in shared memory, and where in the row it lies (k and
+  // real: each lane's first position and how many count).  false: it does not count.
+  static __device__ __forceinline__ bool at(int i, int k, int real, int& place, int& col) {
+    const int from = i / B, e = i % B;
+    place = from * kPitch + e * (int)sizeof(T);
+    col = __shfl_sync(0xFFFFFFFFu, k, from) + e;
+    return e < __shfl_sync(0xFFFFFFFFu, real, from);
+  }
+};
+
+template <int DT, int FMT, bool VEC>
 __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs a) {
   ptx::enter_dependent();
   if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
   using T = typename Elem<DT>::T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using S = Staged<T, B>;
+  __shared__ __align__(16) uint8_t staged[VEC ? 16 : kQWarps * S::kBytes];
+  uint8_t* mine = staged + (VEC ? 0 : warp * S::kBytes);
   const long long batch = blockIdx.z;
   const long long blk = (long long)blockIdx.y * 32 + lane;
   const int row0 = ((int)blockIdx.x >> 2) * kFp4RowTile + ((int)blockIdx.x & 3) * kQWarps + warp;
   T* dst = reinterpret_cast<T*>(a.data) + batch * a.batch_stride;
   const float g = FMT == HINM_FP4_NV && a.g ? __ldg(a.g + batch) : 1.0f;
   int k = 0, real = 0;
-  if (blk >= a.nblk || !depth_place(a, blk * B, B, k, real) || real == 0) return;
+  if (blk >= a.nblk || !depth_place(a, blk * B, B, k, real)) real = 0;
+  if (VEC && real == 0) return;
   uint32_t w[4][B / 8], code[4];
   bool here[4];
 #pragma unroll
@@ -749,7 +807,10 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
     long long tile;
     int at;
     here[j] = row < a.rows && row_place(a, row, tile, at);
-    if (!here[j]) continue;
+    code[j] = 0;
+#pragma unroll
+    for (int i = 0; i < B / 8; ++i) w[j][i] = 0;
+    if (!here[j] || real == 0) continue;
     const uint8_t* in = a.values + (batch * a.rows + row) * a.pitch + blk * (B / 2);
     if constexpr (B == 16) {
       const uint2 t = __ldg(reinterpret_cast<const uint2*>(in));
@@ -769,7 +830,7 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
   for (int j = 0; j < 4; ++j) {
     if (!here[j]) continue;
     const float s = scale_value<FMT>(code[j]);
-    T* out = dst + (long long)(row0 + 32 * j) * a.ld + k;
+    T* row = dst + (long long)(row0 + 32 * j) * a.ld;
 #pragma unroll
     for (int i = 0; i < B / 16; ++i) {
       float v[16];
@@ -777,7 +838,7 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
       for (int h = 0; h < 2; ++h)
         decode8(w[j][2 * i + h], s, g, reinterpret_cast<float(&)[8]>(v[8 * h]));
       constexpr int kOut = 4 * (int)sizeof(T);  // words of 16 elements
-      if (a.vec && real == B) {
+      if (!VEC || real == B) {
         uint32_t u[kOut];
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -788,8 +849,9 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
 #pragma unroll
           for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(v[q]);
         }
-        T* to = out + 16 * i;
-        if (a.vec == 32) {
+        T* to = VEC ? row + k + 16 * i
+                    : reinterpret_cast<T*>(mine + lane * S::kPitch + i * 4 * kOut);
+        if (VEC && a.vec == 32) {
 #pragma unroll
           for (int q = 0; q < kOut; q += 8) store32(reinterpret_cast<uint32_t*>(to) + q, u + q);
         } else {
@@ -801,8 +863,18 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
       } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          if (16 * i + q < real) out[16 * i + q] = Elem<DT>::of(v[q]);
+          if (16 * i + q < real) row[k + 16 * i + q] = Elem<DT>::of(v[q]);
       }
+    }
+    if constexpr (!VEC) {
+      __syncwarp();
+#pragma unroll 8
+      for (int i = lane; i < 32 * B; i += 32) {
+        int place, col;
+        const bool there = S::at(i, k, real, place, col);
+        if (there) row[col] = *reinterpret_cast<const T*>(mine + place);
+      }
+      __syncwarp();
     }
   }
 }
@@ -974,8 +1046,7 @@ __device__ __forceinline__ uint32_t infinite(uint32_t m) {  // some magnitude is
   return (m & 0xFFFFu) >= kInf || (m >> 16) >= kInf;
 }
 
-// This thread's share of a matrix: whole rows of aligned pieces as one run of memory when they
-// are (ld == cols), else row by row.
+// This thread's share of a matrix: rows without gaps (ld == cols) as one run of memory.
 template <int DT, bool FINITE>
 __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batch, int r0, int r1,
                                                int c0, int c1) {
@@ -986,9 +1057,16 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
   const long long threads = (long long)gridDim.x * blockDim.x;
   const long long words = (a.cols + 31) / 32;
   uint32_t m = 0;
-  if (a.vec && a.ld == a.cols && c0 == 0 && c1 == a.cols && (!a.bits || a.cols % 32 == 0)) {
-    const uint4* p = reinterpret_cast<const uint4*>(src + (long long)r0 * a.cols);
-    const long long n = (long long)(r1 - r0) * a.cols / kPer;
+  if (a.ld == a.cols && c0 == 0 && c1 == a.cols && (!a.bits || (a.vec && a.cols % 32 == 0))) {
+    const T* first = src + (long long)r0 * a.cols;
+    const long long all = (long long)(r1 - r0) * a.cols;
+    // elements before the first whole piece (none where rows are aligned) and behind the last
+    const long long head =
+        min(all, (long long)((16 - reinterpret_cast<uintptr_t>(first) % 16) % 16 / sizeof(T)));
+    const uint4* p = reinterpret_cast<const uint4*>(first + head);
+    const long long n = (all - head) / kPer, tail = head + n * kPer;
+    if (tid < head) m = widest16<DT, FINITE>(m, make_uint4(__ldg(first + tid), 0, 0, 0));
+    if (tid < all - tail) m = widest16<DT, FINITE>(m, make_uint4(__ldg(first + tail + tid), 0, 0, 0));
     // whole words of mask a row: the bits run along with the elements, kPer of them a piece
     const uint8_t* bits =
         a.bits ? reinterpret_cast<const uint8_t*>(a.bits + (batch * a.rows + r0) * words) : nullptr;
@@ -1011,23 +1089,30 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
     }
     return m;
   }
-  // warps along the rows, lanes along a row's pieces (elements where they are not aligned)
-  const int lane = threadIdx.x & 31;
-  for (long long row = r0 + (tid >> 5); row < r1; row += threads >> 5) {
-    const T* p = src + row * a.ld;
-    const uint32_t* bits = a.bits ? a.bits + (batch * a.rows + row) * words : nullptr;
-    if (a.vec && c0 == 0 && c1 == a.cols) {
-      for (int c = lane * kPer; c < a.cols; c += 32 * kPer) {
-        uint4 t = __ldg(reinterpret_cast<const uint4*>(p + c));
-        if (bits) t = masked_piece<DT>(t, __ldg(bits + c / 32) >> (c % 32));
-        m = widest16<DT, FINITE>(m, t);
-      }
-    } else {
-      for (int c = c0 + lane; c < c1; c += 32) {
-        if (bits && !((__ldg(bits + c / 32) >> (c % 32)) & 1u)) continue;
-        m = widest16<DT, FINITE>(m, make_uint4(__ldg(p + c), 0, 0, 0));
-      }
+  // rows apart, or not whole pieces: a row's pieces (its elements where they are not aligned), one
+  // after the other over all rows
+  const bool pieces = a.vec && c0 == 0 && c1 == a.cols;
+  const int per = pieces ? a.cols / kPer : c1 - c0;
+  const long long total = (long long)(r1 - r0) * per;
+  for (long long i = tid; i < total; i += kAhead * threads) {
+    uint4 t[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const long long at = i + j * threads;
+      t[j] = make_uint4(0, 0, 0, 0);
+      if (at >= total) continue;
+      const long long row = total < 0x7FFFFFFF ? (uint32_t)at / (uint32_t)per : at / per;
+      const int unit = (int)(at - row * per);
+      const int col = pieces ? unit * kPer : c0 + unit;
+      const T* p = src + (r0 + row) * a.ld + col;
+      uint32_t k = 0xFFFFFFFFu;
+      if (a.bits)
+        k = __ldg(a.bits + (batch * a.rows + r0 + row) * words + col / 32) >> (col % 32);
+      if (pieces) t[j] = masked_piece<DT>(__ldg(reinterpret_cast<const uint4*>(p)), k);
+      else if (k & 1u) t[j].x = __ldg(p);
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) m = widest16<DT, FINITE>(m, t[j]);
   }
   return m;
 }
@@ -1118,7 +1203,10 @@ cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
                     (unsigned)((a.nblk + 31) / 32), (unsigned)batch);
     a.early = few(grid);
     if (back)
-      return launch_kernel(dequant_rows_kernel<DT, FMT>, grid, kQWarps * 32, 0, s, nullptr, a);
+      return a.vec ? launch_kernel(dequant_rows_kernel<DT, FMT, true>, grid, kQWarps * 32, 0, s,
+                                   nullptr, a)
+                   : launch_kernel(dequant_rows_kernel<DT, FMT, false>, grid, kQWarps * 32, 0, s,
+                                   nullptr, a);
     auto kernel = a.ragged == HINM_RAGGED_ROWS
                       ? (a.vec ? quant_rows_kernel<DT, FMT, true, true>
                                : quant_rows_kernel<DT, FMT, false, true>)
