@@ -33,7 +33,6 @@ struct Elem;
 template <>
 struct Elem<HINM_DTYPE_BF16> {
   using T = uint16_t;
-  static __device__ float load(const T* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
   static __device__ T of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
   static __device__ void unpack(uint32_t w, float& a, float& b) {
     a = __uint_as_float(w << 16);
@@ -43,7 +42,6 @@ struct Elem<HINM_DTYPE_BF16> {
 template <>
 struct Elem<HINM_DTYPE_F16> {
   using T = uint16_t;
-  static __device__ float load(const T* p) { return __half2float(__ushort_as_half(__ldg(p))); }
   static __device__ T of(float v) { return __half_as_ushort(__float2half_rn(v)); }
   static __device__ void unpack(uint32_t w, float& a, float& b) {
     a = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFF)));
@@ -53,7 +51,6 @@ struct Elem<HINM_DTYPE_F16> {
 template <>
 struct Elem<HINM_DTYPE_F32> {
   using T = uint32_t;
-  static __device__ float load(const T* p) { return __uint_as_float(__ldg(p)); }
   static __device__ T of(float v) { return __float_as_uint(v); }
 };
 
@@ -78,32 +75,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-// n (<= B) consecutive elements into v, zeros behind them.  vec: p is 16-byte aligned.
-template <int DT, int B>
-__device__ __forceinline__ void load_run(const typename Elem<DT>::T* p, int n, bool vec,
-                                         float (&v)[B]) {
-  if (vec && n == B) {
-    constexpr int kPer = 16 / sizeof(typename Elem<DT>::T);
-    uint4 w[B / kPer];
-#pragma unroll
-    for (int i = 0; i < B / kPer; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-    for (int i = 0; i < B / kPer; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(typename Elem<DT>::T) == 2)
-          Elem<DT>::unpack(u[j], v[i * kPer + 2 * j], v[i * kPer + 2 * j + 1]);
-        else
-          v[i * kPer + j] = __uint_as_float(u[j]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < B; ++i) v[i] = i < n ? Elem<DT>::load(p + i) : 0.0f;
-  }
 }
 
 // ------------------------------------------------------------------ codes
@@ -575,63 +546,54 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
 }
 
 // ------------------------------------------------------------------ depth along the source's columns
-// A thread takes a column of the source (a stored row) and 64 of the depth: 32 bytes of values, one
-// whole sector.
-constexpr int kQDepth = 64;
+constexpr int kQDepth = 64;  // of the depth that a warp takes
 constexpr int kQThreads = 128;
 
-template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) quant_cols_kernel(const QArgs a) {
-  __shared__ ScaleTable table;
-  fill<FMT>(table);
-  ptx::enter_dependent();
-  if (a.early) ptx::launch_dependents();
-  constexpr int B = fp4_block(FMT);
-  using T = typename Elem<DT>::T;
-  const long long batch = blockIdx.z;
-  const int row = (int)blockIdx.x * kQThreads + (int)threadIdx.x;
-  const long long p = (long long)blockIdx.y * kQDepth;
-  const float inv_g = FMT == HINM_FP4_NV && a.g ? __frcp_rn(__ldg(a.g + batch)) : 1.0f;
-  int k = 0, real = 0;
-  if (row >= a.rows || !depth_place(a, p, kQDepth, k, real)) return;
-  const T* src = reinterpret_cast<const T*>(a.data) + batch * a.batch_stride + row;
-  uint32_t w[kQDepth / 8];
-  uint32_t sc = 0;
+// The 16 bytes at p, which is aligned to its elements only: of 16-bit elements the one or two
+// aligned pieces around them (4883 x 3382 bf16 NV 17.9 us, element by element 25); of 32-bit ones,
+// or where the pieces reach out of [lo, hi), the elements inside it.
+template <class T>
+__device__ __forceinline__ uint4 piece_anywhere(const T* p, uintptr_t lo, uintptr_t hi) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  uint32_t u[8];
+  if (sizeof(T) == 2 && at >= lo && at + (shift ? 32 : 16) <= hi) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+    const uint4 y = shift ? __ldg(reinterpret_cast<const uint4*>(at) + 1) : make_uint4(0, 0, 0, 0);
+    u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+    u[4] = y.x, u[5] = y.y, u[6] = y.z, u[7] = y.w;
+    if (shift & 8) {
 #pragma unroll
-  for (int b = 0; b < kQDepth / B; ++b) {
-    float x[B];
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int d = b * B + i;
-      bool keep = d < real;
-      if (keep && a.bits) {
-        const long long words = (a.rows + 31) / 32;
-        keep = (__ldg(a.bits + (batch * a.depth + k + d) * words + row / 32) >> (row % 32)) & 1u;
-      }
-      x[i] = keep ? Elem<DT>::load(src + (long long)(k + d) * a.ld) : 0.0f;
+      for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
     }
-    sc |= encode_block<FMT, B>(table, x, inv_g, reinterpret_cast<uint32_t(&)[B / 8]>(w[b * (B / 8)]))
-          << (8 * b);
+    if (shift & 4) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+    }
+    if (shift & 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
+    }
+  } else {
+    u[0] = u[1] = u[2] = u[3] = 0;
+#pragma unroll
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+      if (reinterpret_cast<uintptr_t>(p + i) + sizeof(T) <= hi) {
+        if constexpr (sizeof(T) == 2) u[i / 2] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+        else u[i] = __ldg(p + i);
+      }
+    }
   }
-  long long tile;
-  int at;
-  if (!row_place(a, row, tile, at)) return;
-  uint4* out = reinterpret_cast<uint4*>(a.values + (batch * a.rows + row) * a.pitch + p / 2);
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  uint8_t* s = a.scales +
-               ((batch * a.row_tiles + tile) * a.chunks + p / (4 * B)) * kFp4ChunkBytes +
-               (at % 32) * 16 + (at / 32) * 4;
-  if constexpr (FMT == HINM_FP4_NV) *reinterpret_cast<uint32_t*>(s) = sc;
-  else *reinterpret_cast<uint16_t*>(s + (p / kQDepth % 2) * 2) = (uint16_t)sc;
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Aligned rows of whole 16-byte pieces: a thread takes one piece's columns (8 of 16 bits, 4 of 32)
+// Rows as 16-byte pieces: a thread takes one piece's columns (8 of 16 bits, 4 of 32)
 // and 16 of the depth, a warp 8 pieces and 64 of the depth, lane = 4 * piece + depth part: the loads
 // of a row part are 128 contiguous bytes, and the 8 bytes that four lanes write for a column are one
 // sector.  A block of 32 lies in two neighbouring lanes.  (Two columns and 64 of the depth a thread,
-// with 4-byte loads, took 22.6 us at 4096 x 4096 bf16 NV and 33.6 us MX; this takes 12.0 and 8.9.)
-template <int DT, int FMT, bool MASK>
+// with 4-byte loads, took 22.6 us at 4096 x 4096 bf16 NV and 33.6 us MX; this takes 11.2 and 8.9.)
+// ALIGNED: rows are aligned and of whole pieces.
+template <int DT, int FMT, bool MASK, bool ALIGNED>
 __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) {
   __shared__ ScaleTable table;
   fill<FMT>(table);
@@ -652,13 +614,17 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) 
   const uint32_t live = __ballot_sync(0xFFFFFFFFu, c0 < a.rows);
   if (c0 >= a.rows || !depth_place(a, p0, kQDepth, k, real)) return;
   const T* src = reinterpret_cast<const T*>(a.data) + batch * a.batch_stride + c0;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(src - c0);
+  const uintptr_t hi = lo + ((unsigned long long)(a.depth - 1) * a.ld + a.rows) * sizeof(T);
   uint32_t u[16][4];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int d = part * 16 + i;
     uint4 t = make_uint4(0, 0, 0, 0);
     if (d < real) {
-      t = __ldg(reinterpret_cast<const uint4*>(src + (long long)(k + d) * a.ld));
+      const T* p = src + (long long)(k + d) * a.ld;
+      if constexpr (ALIGNED) t = __ldg(reinterpret_cast<const uint4*>(p));
+      else t = piece_anywhere(p, lo, hi);
       if constexpr (MASK) {
         const long long words = (a.rows + 31) / 32;
         const uint32_t m = __ldg(a.bits + (batch * a.depth + k + d) * words + c0 / 32) >> (c0 % 32);
@@ -730,7 +696,7 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) 
     const int row = c0 + c;
     long long tile;
     int at;
-    if (a.ragged != HINM_RAGGED_ROWS || row_place(a, row, tile, at))
+    if ((ALIGNED || row < a.rows) && (a.ragged != HINM_RAGGED_ROWS || row_place(a, row, tile, at)))
       *reinterpret_cast<uint2*>(a.values + (batch * a.rows + row) * a.pitch + p0 / 2 + part * 8) =
           make_uint2(w[0], w[1]);
   }
@@ -748,7 +714,7 @@ __global__ void __launch_bounds__(kQThreads) quant_pieces_kernel(const QArgs a) 
     const int row = c0 + 4 * h + part;
     long long tile;
     int at;
-    if (!row_place(a, row, tile, at)) continue;
+    if ((!ALIGNED && row >= a.rows) || !row_place(a, row, tile, at)) continue;
     uint8_t* s = a.scales +
                  ((batch * a.row_tiles + tile) * a.chunks + p0 / (4 * B)) * kFp4ChunkBytes +
                  (at % 32) * 16 + (at / 32) * 4;
@@ -950,6 +916,7 @@ __global__ void __launch_bounds__(kQThreads) dequant_pieces_kernel(const QArgs a
   }
 }
 
+// A thread takes a column (a stored row) and 64 of the depth.
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kQThreads) dequant_cols_kernel(const QArgs a) {
   ptx::enter_dependent();
@@ -1216,22 +1183,22 @@ cudaError_t run_quant(QArgs a, int axis, int batch, bool back, cudaStream_t s) {
   }
   const unsigned ny = (unsigned)(a.nblk * fp4_block(FMT) / kQDepth);
   constexpr int kCols = 16 / es;
-  if (vec && a.rows % kCols == 0) {
-    const int per = kQThreads / 32 * 8 * kCols;
-    const dim3 grid((unsigned)((a.rows + per - 1) / per), ny, (unsigned)batch);
-    a.early = few(grid);
-    if (back)
-      return launch_kernel(dequant_pieces_kernel<DT, FMT>, grid, kQThreads, 0, s, nullptr, a);
-    return a.bits
-               ? launch_kernel(quant_pieces_kernel<DT, FMT, true>, grid, kQThreads, 0, s, nullptr, a)
-               : launch_kernel(quant_pieces_kernel<DT, FMT, false>, grid, kQThreads, 0, s, nullptr,
-                               a);
+  const int per = kQThreads / 32 * 8 * kCols;
+  const dim3 pieces((unsigned)((a.rows + per - 1) / per), ny, (unsigned)batch);
+  const bool whole = vec && a.rows % kCols == 0;
+  if (!back || whole) {
+    a.early = few(pieces);
+    auto kernel = back      ? dequant_pieces_kernel<DT, FMT>
+                  : !a.bits ? (whole ? quant_pieces_kernel<DT, FMT, false, true>
+                                     : quant_pieces_kernel<DT, FMT, false, false>)
+                            : (whole ? quant_pieces_kernel<DT, FMT, true, true>
+                                     : quant_pieces_kernel<DT, FMT, true, false>);
+    return launch_kernel(kernel, pieces, kQThreads, 0, s, nullptr, a);
   }
-  // other rows: element by element, a column a thread
+  // back into other rows: element by element, a column a thread
   const dim3 grid((unsigned)((a.rows + kQThreads - 1) / kQThreads), ny, (unsigned)batch);
   a.early = few(grid);
-  return back ? launch_kernel(dequant_cols_kernel<DT, FMT>, grid, kQThreads, 0, s, nullptr, a)
-              : launch_kernel(quant_cols_kernel<DT, FMT>, grid, kQThreads, 0, s, nullptr, a);
+  return launch_kernel(dequant_cols_kernel<DT, FMT>, grid, kQThreads, 0, s, nullptr, a);
 }
 
 cudaError_t dispatch(const QArgs& a, int dtype, int format, int axis, int batch, bool back,
