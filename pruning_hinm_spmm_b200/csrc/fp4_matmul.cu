@@ -73,7 +73,7 @@ struct MmArgs {
   int dtype, act;
   int q_major;      // Y is [Q][P]: lanes along a row of Y
   int bias_q;       // the bias goes along Q
-  int align;        // 32, 16 or less: alignment of Y's rows
+  int align;        // of Y's rows: a power of two, 32 at most
   int* status;
 };
 
@@ -226,10 +226,11 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Alignment (32, 16 or 0) of Y's elements `at`, `at + ldy`, ... (its rows are `a.align`ed)
+// The power of two (32 at most) that the addresses of Y's elements `at`, `at + ldy`, ... are multiples
+// of.
 __device__ __forceinline__ int align_of(const MmArgs& a, long long at) {
-  const int here = (int)(at * (a.dtype == HINM_DTYPE_F32 ? 4 : 2)) & 31;
-  return here == 0 ? a.align : (here & 15) == 0 ? min(a.align, 16) : 0;
+  const int bits = (int)(at * (a.dtype == HINM_DTYPE_F32 ? 4 : 2)) | a.align;
+  return min(32, bits & -bits);
 }
 
 // The tensor-core instructions, of one CTA or of a pair.
@@ -288,63 +289,46 @@ __device__ __forceinline__ void stage(uint32_t tile, int lane, int c, int dtype,
   }
 }
 
-// The staging tile's first n columns of `rows` rows to Y, from element `at0` on.
-__device__ __forceinline__ void write_tile(const MmArgs& a, uint32_t tile, int lane, int rows,
-                                           int n, long long at0) {
-  const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
-  const int align = align_of(a, at0);
-  char* y0 = reinterpret_cast<char*>(a.Y) + at0 * es;
-  const long long pitch = a.ldy * es;
-  if (align >= 32 && n * es % 32 == 0) {
-    // 32 bytes a lane, a row's 128 in four lanes
-    const int p = (lane & 3) * 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (r < rows && p * 16 < n * es) {
-        const uint4 u = ptx::ld_shared_v4(piece(tile, r, p));
-        const uint4 v = ptx::ld_shared_v4(piece(tile, r, p + 1));
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                         y0 + r * pitch + p * 16),
-                     "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-      }
-    }
-  } else if (align >= 16 && n * es % 16 == 0) {
-    const int p = lane & 7;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      if (r < rows && p * 16 < n * es)
-        *reinterpret_cast<uint4*>(y0 + r * pitch + p * 16) = ptx::ld_shared_v4(piece(tile, r, p));
-    }
-  } else {
-    // rows that start anywhere: element by element, lanes along a row, 8 rows at a time
-    for (int c = lane; c < n; c += 32) {
+// The staging tile's first n columns of `rows` rows to Y, W bytes a lane: as many rows at a time as
+// 32 lanes hold 128 bytes of (narrower stores the less Y's rows are aligned).
+template <class Word>
+__device__ __forceinline__ void write_units(uint32_t tile, int lane, int rows, int bytes, char* y0,
+                                            long long pitch) {
+  constexpr int W = (int)sizeof(Word);
+  constexpr int kLanes = 128 / W < 32 ? 128 / W : 32;  // lanes that write one row
+  constexpr int kRows = 32 / kLanes;
+  const int r0 = lane / kLanes;
 #pragma unroll 1
-      for (int r0 = 0; r0 < min(rows, 32); r0 += 8) {
-        uint32_t v[8];
+  for (int at = lane % kLanes * W; at < bytes; at += kLanes * W) {
+#pragma unroll 1
+    for (int i = 0; i < 32 / kRows && i * kRows < rows; i += 8) {
+      Word v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t from = piece(tile, r0 + i, c * es / 16) + c * es % 16;
-          if (es == 4) {
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[i]) : "r"(from) : "memory");
-          } else {
-            uint16_t h;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(from) : "memory");
-            v[i] = h;
-          }
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int r = (i + j) * kRows + r0;
+        if (i + j < 32 / kRows)
+          v[j] = *reinterpret_cast<const Word*>(__cvta_shared_to_generic(
+              piece(tile, r, at / 16) + at % 16));
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (r0 + i >= rows) continue;
-          char* to = y0 + (r0 + i) * pitch + c * es;
-          if (es == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
-          else *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int r = (i + j) * kRows + r0;
+        if (i + j < 32 / kRows && r < rows) *reinterpret_cast<Word*>(y0 + r * pitch + at) = v[j];
       }
     }
   }
+}
+__device__ __forceinline__ void write_tile(const MmArgs& a, uint32_t tile, int lane, int rows,
+                                           int n, long long at0) {
+  const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
+  const int bytes = n * es, unit = align_of(a, at0) | (bytes & 15 ? bytes : 16);
+  char* y0 = reinterpret_cast<char*>(a.Y) + at0 * es;
+  const long long pitch = a.ldy * es;
+  const int low = unit & -unit;  // the largest power of two that divides rows' places and lengths
+  if (low >= 16) write_units<uint4>(tile, lane, rows, bytes, y0, pitch);
+  else if (low == 8) write_units<uint2>(tile, lane, rows, bytes, y0, pitch);
+  else if (low == 4) write_units<uint32_t>(tile, lane, rows, bytes, y0, pitch);
+  else write_units<uint16_t>(tile, lane, rows, bytes, y0, pitch);
 }
 
 // COLS columns of whole 32-byte aligned rows of Y: what a tile inside Y takes.  Lane l brings row l
@@ -1097,7 +1081,7 @@ cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out
   const long long es = o.dtype == HINM_DTYPE_F32 ? 4 : 2;
   const unsigned long long bits =
       reinterpret_cast<uintptr_t>(o.Y) | (uintptr_t)(o.ldy * es) | (uintptr_t)(o.batch_stride * es);
-  a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
+  a.align = (int)((bits | 32) & (~(bits | 32) + 1));
   a.status = status;
   return A.format == HINM_FP4_NV ? pick<HINM_FP4_NV>(a, A, B, o.transposed != 0, s)
                                  : pick<HINM_FP4_MX>(a, A, B, o.transposed != 0, s);
