@@ -264,31 +264,6 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int p) {
   return tile + r * 128 + ((p ^ (r & 7)) << 4);
 }
 
-// A lane's 16 columns, from column c (a multiple of 16) of the staging tile on, in Y's type.
-__device__ __forceinline__ void stage(uint32_t tile, int lane, int c, int dtype,
-                                      const float (&y)[kEpiCols]) {
-  if (dtype == HINM_DTYPE_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ptx::st_shared_v4(piece(tile, lane, c / 4 + i), __float_as_uint(y[4 * i]),
-                        __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
-                        __float_as_uint(y[4 * i + 3]));
-  } else {
-    uint32_t u[8];
-    if (dtype == HINM_DTYPE_BF16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = pack_f16(y[2 * i], y[2 * i + 1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      ptx::st_shared_v4(piece(tile, lane, c / 8 + i), u[4 * i], u[4 * i + 1], u[4 * i + 2],
-                        u[4 * i + 3]);
-  }
-}
-
 // The staging tile's first n columns of `rows` rows to Y, W bytes a lane: as many rows at a time as
 // 32 lanes hold 128 bytes of (narrower stores the less Y's rows are aligned).
 template <class Word>
@@ -331,22 +306,11 @@ __device__ __forceinline__ void write_tile(const MmArgs& a, uint32_t tile, int l
   else write_units<uint16_t>(tile, lane, rows, bytes, y0, pitch);
 }
 
-// COLS columns of whole 32-byte aligned rows of Y: what a tile inside Y takes.  Lane l brings row l
-// of the accumulator at `acc`; all of its columns are read first, and `done` is called, so that the
-// accumulator is free while they are worked on, PC of them (64 or 128 bytes) at a time.  rows: how
-// many count; y: element 0 of row 0 of Y.
-template <int DT, int COLS, bool BIASQ, class Done>
-__device__ __forceinline__ void write_columns(const MmArgs& a, uint32_t acc, bool zero, float alpha,
-                                              float bias_row, const float* bias_cols,
-                                              uint32_t tile, int lane, int rows, char* y,
-                                              Done done) {
-  constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
-  constexpr int PC = DT != HINM_DTYPE_F32 && COLS % 64 == 0 ? 64 : 32;
-  constexpr int kLanes = PC * es / 32;  // lanes that write one row, 32 bytes each
-  constexpr int kRows = 32 / kLanes;    // rows of one store
-  uint32_t v[COLS];
+// N columns of the accumulator into registers (zero: there were no products).
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t acc, bool zero, uint32_t (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < COLS; i += 32) {
+  for (int i = 0; i < N; i += 32) {
     if (!zero) {
       ptx::tmem_ld_32x32b_x32(acc + i, reinterpret_cast<uint32_t(&)[32]>(v[i]));
     } else {
@@ -355,43 +319,81 @@ __device__ __forceinline__ void write_columns(const MmArgs& a, uint32_t acc, boo
     }
   }
   ptx::tmem_ld_wait();
-  done();
-  // places in the staging tile (piece()): of this lane's row, and of what it writes out (a row's
-  // number mod 8 does not change from store to store)
-  const uint32_t in = tile + lane * 128 + ((lane & 7) << 4);
-  const int r0 = lane / kLanes, p0 = (lane % kLanes) * 2;
-  const uint32_t out = tile + r0 * 128 + ((p0 ^ (r0 & 7)) << 4);
+}
+
+// What goes with a warp's columns of one tile.
+struct Columns {
+  float alpha, bias_row;
+  const float* bias_cols;
+  uint32_t tile;  // the warp's staging tile
+  int lane;       // brings row `lane`
+  int rows, cols; // how many count
+  long long at0;  // element 0 of row 0 in Y
+};
+
+// PC columns (64 or 128 bytes of Y), from column `col` on, into the staging tile.
+template <int DT, int PC, bool BIASQ, bool LINES>
+__device__ __forceinline__ void stage_columns(const MmArgs& a, const Columns& c, int col,
+                                              const uint32_t* v) {
+  constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
+  const uint32_t in = c.tile + c.lane * 128 + ((c.lane & 7) << 4);  // this lane's row (piece())
+#pragma unroll
+  for (int h = 0; h < PC; h += kEpiCols) {
+    float f[kEpiCols];
+#pragma unroll
+    for (int i = 0; i < kEpiCols; ++i)
+      f[i] = fmaf(__uint_as_float(v[h + i]), c.alpha,
+                  BIASQ ? __ldg(c.bias_cols + (LINES ? col + h + i : min(col + h + i, c.cols - 1)))
+                        : c.bias_row);
+    if (a.act == HINM_ACT_NONE) {
+    } else if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU>(f);
+    else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU>(f);
+    else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU>(f);
+#pragma unroll
+    for (int i = 0; i < kEpiCols * es / 16; ++i) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u[j] = DT == HINM_DTYPE_F32    ? __float_as_uint(f[4 * i + j])
+               : DT == HINM_DTYPE_BF16 ? pack_bf16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1])
+                                       : pack_f16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1]);
+      ptx::st_shared_v4(in ^ (uint32_t)(h * es + 16 * i), u[0], u[1], u[2], u[3]);
+    }
+  }
+}
+
+// COLS columns that all count, of rows that are 32-byte aligned.  HOLD (one accumulator): all are
+// read first, and `done` is called, so that the accumulator is free while they are worked on (pairs
+// at 11008 x 4096 x 4096: 86.8 us, else 89.5).
+template <int DT, int COLS, bool BIASQ, bool HOLD, class Done>
+__device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool zero,
+                                            const Columns& c, Done done) {
+  constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
+  constexpr int PC = DT != HINM_DTYPE_F32 && COLS % 64 == 0 ? 64 : 32;
+  constexpr int kLanes = PC * es / 32;  // lanes that write one row, 32 bytes each
+  constexpr int kRows = 32 / kLanes;    // rows of one store
+  uint32_t v[HOLD ? COLS : PC];
+  if constexpr (HOLD) {
+    read_columns<COLS>(acc, zero, v);
+    done();
+  }
+  // what this lane writes out: its row's number mod 8 does not change from store to store
+  const int r0 = c.lane / kLanes, p0 = (c.lane % kLanes) * 2;
+  const uint32_t out = c.tile + r0 * 128 + ((p0 ^ (r0 & 7)) << 4);
   const long long pitch = a.ldy * es;
-  char* yr = y + r0 * pitch + p0 * 16;
+  char* yr = reinterpret_cast<char*>(a.Y) + c.at0 * es + r0 * pitch + p0 * 16;
 #pragma unroll
   for (int col = 0; col < COLS; col += PC) {
-#pragma unroll
-    for (int h = 0; h < PC; h += kEpiCols) {
-      float f[kEpiCols];
-#pragma unroll
-      for (int i = 0; i < kEpiCols; ++i)
-        f[i] = fmaf(__uint_as_float(v[col + h + i]), alpha,
-                    BIASQ ? __ldg(bias_cols + col + h + i) : bias_row);
-      if (a.act == HINM_ACT_NONE) {
-      } else if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU>(f);
-      else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU>(f);
-      else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU>(f);
-#pragma unroll
-      for (int i = 0; i < kEpiCols * es / 16; ++i) {
-        uint32_t u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          u[j] = DT == HINM_DTYPE_F32    ? __float_as_uint(f[4 * i + j])
-                 : DT == HINM_DTYPE_BF16 ? pack_bf16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1])
-                                         : pack_f16(f[8 * i + 2 * j], f[8 * i + 2 * j + 1]);
-        ptx::st_shared_v4(in ^ (uint32_t)(h * es + 16 * i), u[0], u[1], u[2], u[3]);
-      }
+    if constexpr (!HOLD) {
+      read_columns<PC>(acc + col, zero, v);
+      if (col + PC >= COLS) done();
     }
+    stage_columns<DT, PC, BIASQ, true>(a, c, col, HOLD ? v + col : v);
     __syncwarp();
     char* yo = yr + col * es;
 #pragma unroll
     for (int i = 0; i < 32 / kRows; ++i) {
-      if (r0 + i * kRows < rows) {
+      if (r0 + i * kRows < c.rows) {
         const uint4 u = ptx::ld_shared_v4(out + i * kRows * 128);
         const uint4 w = ptx::ld_shared_v4((out ^ 16) + i * kRows * 128);
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(yo), "r"(u.x),
@@ -400,6 +402,24 @@ __device__ __forceinline__ void write_columns(const MmArgs& a, uint32_t acc, boo
       }
       yo += kRows * pitch;
     }
+    __syncwarp();
+  }
+}
+
+// Any columns and rows: read as they are worked on (beside write_lines' held columns, holding these
+// too made the kernel of pairs spill).
+template <int DT, int COLS, bool BIASQ, class Done>
+__device__ __forceinline__ void write_any(const MmArgs& a, uint32_t acc, bool zero,
+                                          const Columns& c, Done done) {
+  constexpr int PC = DT != HINM_DTYPE_F32 && COLS % 64 == 0 ? 64 : 32;
+#pragma unroll 1
+  for (int col = 0; col < c.cols; col += PC) {
+    uint32_t v[PC];
+    read_columns<PC>(acc + col, zero, v);
+    if (col + PC >= c.cols) done();
+    stage_columns<DT, PC, BIASQ, false>(a, c, col, v);
+    __syncwarp();
+    write_tile(a, c.tile, c.lane, c.rows, min(PC, c.cols - col), c.at0 + col);
     __syncwarp();
   }
 }
@@ -728,25 +748,28 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       ptx::tc_fence_after();
       const long long y0 = a.ragged == HINM_RAGGED_DEPTH ? w.e * a.y_batch : 0;
       const int col0 = part * kOwn, col1 = min(w.q_len, col0 + kOwn);
-      const uint32_t tile = ptx::smem_u32(epi_smem + (warp - 2) * kEpiTile);
-      const int pass = a.dtype == HINM_DTYPE_F32 ? 32 : 64;  // columns of the staging tile
       const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * C::kAccCols);
       if constexpr (!SPLIT) {
-        const int es = a.dtype == HINM_DTYPE_F32 ? 4 : 2;
-        const long long at0 = y0 + (long long)(w.p_out + quad * 32) * a.ldy + w.q_out + col0;
-        if (!a.q_major && w.q_len == BN && align_of(a, at0) == 32) {
-          const float* bias_cols = bias && a.bias_q ? bias + w.q_out + col0 : nullptr;
-          char* y = reinterpret_cast<char*>(a.Y) + at0 * es;
-          const int rows = w.p_len - quad * 32;
+        if (!a.q_major && col0 < col1) {
+          const Columns cw{alpha,
+                           bias_p,
+                           bias && a.bias_q ? bias + w.q_out + col0 : nullptr,
+                           ptx::smem_u32(epi_smem + (warp - 2) * kEpiTile),
+                           lane,
+                           w.p_len - quad * 32,
+                           col1 - col0,
+                           y0 + (long long)(w.p_out + quad * 32) * a.ldy + w.q_out + col0};
+          const bool lines = cw.cols == kOwn && align_of(a, cw.at0) == 32;
           auto done = [&] { release(b); };
           auto write = [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
-            if (bias_cols)
-              write_columns<DT, kOwn, true>(a, lanes + col0, s1 == s0, alpha, bias_p, bias_cols,
-                                            tile, lane, rows, y, done);
-            else
-              write_columns<DT, kOwn, false>(a, lanes + col0, s1 == s0, alpha, bias_p, nullptr,
-                                             tile, lane, rows, y, done);
+            if (cw.bias_cols) {
+              if (lines) write_lines<DT, kOwn, true, C::kAccBufs == 1>(a, lanes + col0, s1 == s0, cw, done);
+              else write_any<DT, kOwn, true>(a, lanes + col0, s1 == s0, cw, done);
+            } else {
+              if (lines) write_lines<DT, kOwn, false, C::kAccBufs == 1>(a, lanes + col0, s1 == s0, cw, done);
+              else write_any<DT, kOwn, false>(a, lanes + col0, s1 == s0, cw, done);
+            }
           };
           if (a.dtype == HINM_DTYPE_BF16) write(std::integral_constant<int, HINM_DTYPE_BF16>{});
           else if (a.dtype == HINM_DTYPE_F16) write(std::integral_constant<int, HINM_DTYPE_F16>{});
@@ -783,35 +806,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
               part_sums[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         } else {
+          // Y as [Q][P] (then the bias goes along P)
           float y[kEpiCols];
-          if (bias && a.bias_q) {
 #pragma unroll
-            for (int i = 0; i < kEpiCols; ++i)
-              y[i] = fmaf(__uint_as_float(v[i]), alpha,
-                          i < n ? __ldg(bias + w.q_out + col + i) : 0.0f);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kEpiCols; ++i) y[i] = fmaf(__uint_as_float(v[i]), alpha, bias_p);
-          }
+          for (int i = 0; i < kEpiCols; ++i) y[i] = fmaf(__uint_as_float(v[i]), alpha, bias_p);
           if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU>(y);
           else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU>(y);
           else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU>(y);
-          if (a.q_major) {
 #pragma unroll
-            for (int i = 0; i < kEpiCols; ++i)
-              if (i < n && mine)
-                store_one(a.Y, a.dtype,
-                          y0 + (long long)(w.q_out + col + i) * a.ldy + w.p_out + row, y[i]);
-          } else {
-            const int c = (col - col0) & (pass - 1);
-            stage(tile, lane, c, a.dtype, y);
-            if (last || c + kEpiCols == pass) {
-              __syncwarp();
-              write_tile(a, tile, lane, w.p_len - quad * 32, c + n,
-                         y0 + (long long)(w.p_out + quad * 32) * a.ldy + w.q_out + col - c);
-              __syncwarp();
-            }
-          }
+          for (int i = 0; i < kEpiCols; ++i)
+            if (i < n && mine)
+              store_one(a.Y, a.dtype,
+                        y0 + (long long)(w.q_out + col + i) * a.ldy + w.p_out + row, y[i]);
         }
         if (!last && s1 > s0) ptx::tmem_ld_wait();
       }
