@@ -8,6 +8,7 @@ this package raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -166,6 +167,17 @@ def _current(t, name: str, stream=None) -> Tuple[int, int]:
     if dev < 0 or dev != C._cuda_getDevice():
         raise ValueError(f"{name}: need a tensor on the current CUDA device, got {t.device}")
     return dev, (C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream))
+
+
+def _on(stream, device: int):
+    """What a call allocates or fills itself belongs to the stream that it runs on: a tensor of the
+    current stream would be filled, or still be in use by its last owner, unordered with `stream`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t) -> Optional[int]:
@@ -586,19 +598,21 @@ class Fp4Matrix:
 
     @classmethod
     def allocate(cls, format: int, batch: int, rows: int, depth: int, device,
-                 ragged: int = HINM_RAGGED_NONE, offsets=None) -> "Fp4Matrix":
+                 ragged: int = HINM_RAGGED_NONE, offsets=None,
+                 tensor_scale: bool = True) -> "Fp4Matrix":
+        """New buffers; ``tensor_scale``: HINM_FP4_NV gets one too (ones)."""
         torch = _torch()
         groups = 0 if ragged == HINM_RAGGED_NONE or offsets is None else offsets.numel() - 1
         v, s = hinm_fp4_size(format, batch, rows, depth, ragged, groups)
         return cls(format=format, batch=batch, rows=rows, depth=depth,
                    values=_empty_bytes(v, device), scales=_empty_bytes(s, device),
                    tensor_scale=(torch.ones(batch, dtype=torch.float32, device=device)
-                                 if format == HINM_FP4_NV else None),
+                                 if format == HINM_FP4_NV and tensor_scale else None),
                    ragged=ragged, offsets=offsets)
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        object.__setattr__(self, "_c", None)  # as_c() checks and builds again
+        object.__setattr__(self, "_c", (None, None))  # as_c() checks and builds again
 
     def as_c(self, device: Optional[int] = None) -> hinm_fp4:
         """The C struct of the buffers as they are now.  Checks that they are what it says; the
@@ -607,8 +621,9 @@ class Fp4Matrix:
         if device is None:
             device = _torch().cuda.current_device()
         at = (device, v.data_ptr(), s.data_ptr(), _ptr(g), _ptr(o))
-        if self._c is not None and self._at == at:
-            return self._c
+        was, c = self._c
+        if was == at:
+            return c
         torch = _torch()
         vn, sn = hinm_fp4_size(self.format, self.batch, self.rows, self.depth, self.ragged,
                                self.groups)
@@ -616,14 +631,10 @@ class Fp4Matrix:
                                (g, torch.float32, self.batch, "tensor_scale"),
                                (o, torch.int32, 0, "offsets")):
             if t is not None:
-                _device_tensor(t, name, device)
-                if t.dtype != dt or not t.is_contiguous() or t.numel() < n:
-                    raise ValueError(f"Fp4Matrix.{name}: need a contiguous {dt} tensor of at "
-                                     f"least {n} elements")
+                _fp4_buffer(t, dt, n, name, device)
         c = hinm_fp4(HINM_FP4_LAYOUT_VERSION, self.format, self.batch, self.rows, self.depth,
                      self.ragged, self.groups, at[4], at[1], at[2], at[3])
-        object.__setattr__(self, "_at", at)
-        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_c", (at, c))
         return c
 
 
@@ -631,6 +642,13 @@ def _device_tensor(t, name: str, device: int) -> None:
     """Kernels run on the current device: a tensor elsewhere is refused."""
     if t.get_device() != device:
         raise ValueError(f"{name}: need a tensor on the current CUDA device, got {t.device}")
+
+
+def _fp4_buffer(t, dtype, n: int, name: str, device: int) -> None:
+    _device_tensor(t, name, device)
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"Fp4Matrix.{name}: need a contiguous {dtype} tensor of at least {n} "
+                         f"elements")
 
 
 _dtype_codes = {}
@@ -707,37 +725,47 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
     is, or "amax": found on the device from src (hinm_fp4_tensor_scale).  ``bitmask``: hinm_mask's
     words over src; elements whose bit is 0 count as 0.  ``ragged`` and ``offsets`` (int32
     [groups + 1] on the device): tokens sorted by expert along the rows or along the depth.
-    ``out``: a matrix of the same sizes to write into."""
+    ``out``: a matrix of the same sizes to write into.  What the call allocates itself belongs to
+    ``stream``."""
     dev, s = _current(src, "src", stream)
     code, b, r, c, ld, bs = _matrix(src, "src")
+    # every check comes before the first change of `out`: a refused call leaves it as it was
     _fp4_check_mask(bitmask, b, r, c, dev)
-    if out is None:
-        rows, depth = (r, c) if axis == 1 else (c, r)
-        if ragged != HINM_RAGGED_NONE and offsets is None:
-            raise ValueError("a ragged matrix needs offsets")
-        out = Fp4Matrix.allocate(format, b, rows, depth, src.device, ragged, offsets)
-    else:
-        if out.format != format or out.ragged != ragged:
-            raise ValueError("out has another format or ragged form")
-        if ragged != HINM_RAGGED_NONE:
-            if offsets is None or offsets.numel() != out.offsets.numel():
-                raise ValueError("offsets: need as many as out was made for")
-            if out.offsets is not offsets:
-                out.offsets = offsets
-    _fp4_check_source(out, b, r, c, axis)
     amax = isinstance(tensor_scale, str)
     if amax and tensor_scale != "amax":
         raise ValueError(f"tensor_scale={tensor_scale!r}: need None, a tensor or 'amax'")
+    if format != HINM_FP4_NV and tensor_scale is not None:
+        raise ValueError("HINM_FP4_MX has no tensor scale")
+    if ragged != HINM_RAGGED_NONE and offsets is None:
+        raise ValueError("a ragged matrix needs offsets")
+    if out is None:
+        rows, depth = (r, c) if axis == 1 else (c, r)
+        with _on(stream, dev):
+            out = Fp4Matrix.allocate(format, b, rows, depth, src.device, ragged, offsets,
+                                     tensor_scale=False)
+        _fp4_check_source(out, b, r, c, axis)
+    else:
+        if out.format != format or out.ragged != ragged:
+            raise ValueError("out has another format or ragged form")
+        _fp4_check_source(out, b, r, c, axis)
+        moved = ragged != HINM_RAGGED_NONE and out.offsets is not offsets
+        if moved:
+            if offsets.numel() != out.offsets.numel():
+                raise ValueError("offsets: need as many as out was made for")
+            _fp4_buffer(offsets, _torch().int32, 0, "offsets", dev)
+        if tensor_scale is not None and not amax and out.tensor_scale is not tensor_scale:
+            _fp4_buffer(tensor_scale, _torch().float32, b, "tensor_scale", dev)
+        if moved:
+            out.offsets = offsets
     if format == HINM_FP4_NV:
         if not amax:
             if out.tensor_scale is not tensor_scale:
                 out.tensor_scale = tensor_scale
         elif out.tensor_scale is None or out.given_scale:
-            out.tensor_scale = _torch().empty(b, dtype=_torch().float32, device=src.device)
+            with _on(stream, dev):
+                out.tensor_scale = _torch().empty(b, dtype=_torch().float32, device=src.device)
         if out.given_scale == amax:
             out.given_scale = not amax
-    elif tensor_scale is not None:
-        raise ValueError("HINM_FP4_MX has no tensor scale")
     cq, p, m = ctypes.byref(out.as_c(dev)), src.data_ptr(), _ptr(bitmask)
     if amax:
         _check(_lib.hinm_fp4_tensor_scale(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_tensor_scale")
@@ -755,7 +783,8 @@ def hinm_fp4_dequantize(q: Fp4Matrix, axis: int = 1, out=None, dtype=None, strea
         shape = (r, c) if q.batch == 1 else (q.batch, r, c)
         # a ragged matrix leaves places outside its groups as they are
         make = torch.empty if q.ragged == HINM_RAGGED_NONE else torch.zeros
-        out = make(shape, dtype=dtype or torch.bfloat16, device=q.values.device)
+        with _on(stream, dev):
+            out = make(shape, dtype=dtype or torch.bfloat16, device=q.values.device)
     _device_tensor(out, "out", dev)
     code, ob, orow, ocol, ld, bs = _matrix(out, "out")
     _fp4_check_source(q, ob, orow, ocol, axis)
@@ -765,12 +794,13 @@ def hinm_fp4_dequantize(q: Fp4Matrix, axis: int = 1, out=None, dtype=None, strea
 
 
 # ----------------------------------------------------------------------------- b2, b3
-def _fp4_out(Y_out, shape, dtype, like, device: int, zero: bool = False):
-    """Y_out, or a new tensor, with its C arguments (pointer, dtype, ldy, batch stride)."""
+def _fp4_out(Y_out, shape, dtype, like, device: int, stream, zero: bool = False):
+    """Y_out, or a new tensor, with its C arguments (dtype, ldy, batch stride)."""
     if Y_out is None:
         torch = _torch()
-        Y_out = (torch.zeros if zero else torch.empty)(shape, dtype=dtype or torch.bfloat16,
-                                                       device=like.device)
+        with _on(stream, device):
+            Y_out = (torch.zeros if zero else torch.empty)(shape, dtype=dtype or torch.bfloat16,
+                                                           device=like.device)
     if Y_out.shape != shape:
         raise ValueError(f"Y_out: shape {tuple(Y_out.shape)}, need {tuple(shape)}")
     _device_tensor(Y_out, "Y_out", device)
@@ -793,7 +823,7 @@ def hinm_fp4_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None, transpos
     ``dtype``, or Y_out's).  A: the weight, B: the tokens, quantised along the same depth."""
     dev, s = _current(A.values, "A", stream)
     shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
-    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev)
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev, stream)
     _check(_lib.hinm_fp4_matmul(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
                                 Y_out.data_ptr(), code, ldy, 1 if transposed else 0,
                                 _fp4_bias(bias, A.rows, dev), activation, s), "hinm_fp4_matmul")
@@ -808,7 +838,7 @@ def hinm_fp4_grouped_matmul(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=None,
     when it is made here).  bias: fp32 [experts, A.rows] or None."""
     dev, s = _current(A.values, "A", stream)
     shape = (B.rows, A.rows) if transposed else (A.rows, B.rows)
-    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev, zero=True)
+    Y_out, code, ldy, _ = _fp4_out(Y_out, shape, dtype, A.values, dev, stream, zero=True)
     _check(_lib.hinm_fp4_grouped_matmul(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
                                         Y_out.data_ptr(), code, ldy, 1 if transposed else 0,
                                         _fp4_bias(bias, A.batch * A.rows, dev), activation, s),
@@ -821,7 +851,7 @@ def hinm_fp4_grouped_weight_grad(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=N
     its part of A's and B's ragged depth; zeros for a group without tokens."""
     dev, s = _current(A.values, "A", stream)
     shape = (B.groups, A.rows, B.rows)
-    Y_out, code, ldy, bs = _fp4_out(Y_out, shape, dtype or _torch().float32, A.values, dev)
+    Y_out, code, ldy, bs = _fp4_out(Y_out, shape, dtype or _torch().float32, A.values, dev, stream)
     if B.groups == 1:
         bs = (A.rows - 1) * ldy + B.rows
     _check(_lib.hinm_fp4_grouped_weight_grad(ctypes.byref(A.as_c(dev)), ctypes.byref(B.as_c(dev)),
