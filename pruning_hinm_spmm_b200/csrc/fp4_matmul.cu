@@ -189,7 +189,7 @@ __device__ __forceinline__ Tile tile_of(const MmArgs& a, const int* cum, int t, 
 
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
-  if constexpr (ACT == HINM_ACT_RELU) return fmaxf(x, 0.0f);
+  if constexpr (ACT == HINM_ACT_RELU) return ptx::max_nan(x, 0.0f);  // NaN stays NaN
   // The quick exponential is 2 + 1.173 |x| units in the last place off, the quotient 2: of x itself
   // no more than 16 2^-24, as |SiLU(x)| falls with exp(x) where x < 0 and exp(-x) vanishes beside 1
   // where x > 0.  (A correctly rounded division branches, element by element.)

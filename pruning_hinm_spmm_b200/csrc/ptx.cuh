@@ -37,14 +37,15 @@ __device__ __forceinline__ int perm_at(const int32_t* perm, int j, int K) {
 }
 
 // ---------------------------------------------------------------- dependent launches
-// First statement of every kernel of the path (they are launched with programmatic stream
-// serialization, launch.cuh): wait until the kernels this one depends on have finished and
-// their writes are visible.  Every global access of the kernel comes after the wait, so the
-// accesses keep plain stream order; what overlaps is the launch of this kernel with the end
-// of the previous one.  Without a programmatic dependency the wait returns at once.
-// No kernel triggers its dependents early (griddepcontrol.launch_dependents): blocks of
-// the next kernel placed during this one's last wave crowd onto the SMs that are free at
-// that moment, which made the decode step slower (measured on B200: 414 -> 437 us).
+// In every kernel of the library (they are launched with programmatic stream serialization,
+// launch.cuh), before its first access to global memory: wait until the kernels this one
+// depends on have finished and their writes are visible, so the accesses keep plain stream
+// order; what overlaps is the launch of this kernel, and what it sets up on the chip, with the
+// end of the previous one.  Without a programmatic dependency the wait returns at once.
+// Only the 4-bit quantiser's kernels trigger their dependents early (below), and only when
+// their blocks leave SMs free: blocks of the next kernel placed during a full one's last wave
+// crowd onto the SMs that are free at that moment, which made the pruning path's decode step
+// slower (measured on B200: 414 -> 437 us).
 __device__ __forceinline__ void enter_dependent() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -54,6 +55,13 @@ __device__ __forceinline__ void enter_dependent() {
 // most of the SMs free.
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // ---------------------------------------------------------------- cp.async (16-, 8-, 4-byte)

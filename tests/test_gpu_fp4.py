@@ -212,12 +212,12 @@ def test_batch(H, fmt, axis):
 
 
 GROUPS = [[0, 5], [0, 0, 3, 3, 40], [2, 2, 130, 300, 300], [0, 128, 256, 384], [0, 1, 2, 3, 4, 300], [7, 7, 7]]
+MANY = [[0, 700, 701, 1500, 2000], [11, 11, 1290]]
 
 
 @FORMATS
 @pytest.mark.parametrize("axis", [1, 0])
-@pytest.mark.parametrize("o", GROUPS, ids=str)
-@pytest.mark.parametrize("depth", [64, 200])
+@pytest.mark.parametrize("depth,o", [(d, o) for d in (64, 200) for o in GROUPS] + [(900, o) for o in MANY], ids=str)
 def test_ragged_rows(H, fmt, axis, o, depth):
     T = o[-1] + 9
     x = rand(T, T, depth)
@@ -258,8 +258,7 @@ def test_ragged_rows(H, fmt, axis, o, depth):
 
 @FORMATS
 @pytest.mark.parametrize("axis", [1, 0])
-@pytest.mark.parametrize("o", GROUPS, ids=str)
-@pytest.mark.parametrize("rows", [24, 131])
+@pytest.mark.parametrize("rows,o", [(r, o) for r in (24, 131) for o in GROUPS] + [(516, o) for o in MANY], ids=str)
 def test_ragged_depth(H, fmt, axis, o, rows):
     T = o[-1] + 9
     x = rand(T + 1, T, rows)             # tokens x rows: axis 0
@@ -288,6 +287,64 @@ def test_ragged_depth(H, fmt, axis, o, rows):
         if o[e + 1] > o[e]:
             want = F.rounded(np64(x)[o[e]:o[e + 1]].T, fmt, gv).T
             assert same(got[o[e]:o[e + 1]], to_type(want, torch.bfloat16))
+
+
+def mask_words(keep):
+    """bool [..., rows, cols] -> hinm_mask's words."""
+    cols = keep.shape[-1]
+    pad = torch.zeros(*keep.shape[:-1], -(-cols // 32) * 32, dtype=torch.long, device="cuda")
+    pad[..., :cols] = keep
+    words = (pad.unflatten(-1, (-1, 32)) << torch.arange(32, device="cuda")).sum(-1)
+    return torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
+
+
+@FORMATS
+@pytest.mark.parametrize("axis", [1, 0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols,offset,extra", [(640, 1216, 0, 0), (645, 1219, 0, 0), (645, 1219, 3, 2),
+                                                    (512, 1024, 1, 7), (700, 1000, 8, 16)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_many_blocks(H, fmt, axis, dtype, rows, cols, offset, extra, masked):
+    """Several blocks of threads in each direction; rows that start at any element."""
+    big = torch.full((rows, offset + cols + extra), float("nan"), dtype=DT[dtype], device="cuda")
+    x = big[:, offset:offset + cols]
+    x.copy_(rand(rows + cols, rows, cols, dtype=DT[dtype]))
+    keep = torch.ones(rows, cols, dtype=torch.bool, device="cuda")
+    if masked:
+        keep = torch.rand(rows, cols, generator=gen(6), device="cuda") < 0.3
+        x[~keep] = float("nan")
+    q = H.hinm_fp4_quantize(x, fmt, axis=axis, bitmask=mask_words(keep) if masked else None,
+                            tensor_scale="amax" if fmt == F.NV else None)
+    m = np.where(keep.cpu().numpy(), np64(x), 0.0)
+    m = m if axis == 1 else m.T
+    gv = F.pow2_scale(m) if fmt == F.NV else 1.0
+    if fmt == F.NV:
+        assert float(q.tensor_scale) == gv
+    codes, sc = F.quantize(m, fmt, gv)
+    check_stored(q, fmt, codes, sc, m.shape[1])
+    want = F.values(codes, sc, fmt, m.shape[1], gv)
+    back = torch.full_like(big, -3.0)
+    H.hinm_fp4_dequantize(q, axis=axis, out=back[:, offset:offset + cols])
+    assert same(back[:, offset:offset + cols], to_type(want if axis == 1 else want.T, DT[dtype]))
+    assert back[:, :offset].eq(-3).all() and back[:, offset + cols:].eq(-3).all()
+
+
+@FORMATS
+@pytest.mark.parametrize("axis", [1, 0])
+def test_masked_batch(H, fmt, axis):
+    E, R, C = 3, 150, 75
+    x = rand(2, E, R, C, dtype=torch.float32)
+    keep = torch.rand(E, R, C, generator=gen(3), device="cuda") < 0.5
+    x[~keep] = float("inf")
+    keep[1] = False                     # an expert without any weight
+    q = H.hinm_fp4_quantize(x, fmt, axis=axis, bitmask=mask_words(keep), tensor_scale="amax" if fmt == F.NV else None)
+    y = H.hinm_fp4_dequantize(q, axis=axis, dtype=torch.float32)
+    assert y[1].eq(0).all()
+    for e in range(E):
+        m = np.where(keep[e].cpu().numpy(), np64(x[e]), 0.0)
+        m = m if axis == 1 else m.T
+        want = F.rounded(m, fmt, F.pow2_scale(m) if fmt == F.NV else 1.0)
+        assert same(y[e], to_type(want if axis == 1 else want.T, torch.float32))
 
 
 # ----------------------------------------------------------------------------- products
@@ -405,6 +462,50 @@ def test_nan_stays_in_its_row_and_column(H, fmt, M, N, K):
     nan = torch.zeros(M, N, dtype=torch.bool, device="cuda")
     nan[17], nan[:, 33] = True, True
     assert torch.equal(y.isnan(), nan)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["MN", "NM"])
+@pytest.mark.parametrize("act", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N,K", [(300, 40, 300), (256, 4, 4096), (512, 640, 512), (2304, 2112, 256)])
+def test_nan_passes_every_activation(H, transposed, act, M, N, K):
+    w, x = rand(1, M, K), rand(2, N, K)
+    w[17, 5] = float("nan")
+    A, B = H.hinm_fp4_quantize(w, F.MX), H.hinm_fp4_quantize(x, F.MX)
+    bias = torch.zeros(M, device="cuda")
+    bias[20] = float("nan")
+    y = H.hinm_fp4_matmul(A, B, transposed=transposed, bias=bias, activation=act)
+    y = y.t() if transposed else y
+    nan = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    nan[17], nan[20] = True, True
+    assert torch.equal(y.isnan(), nan)
+
+
+def test_places_past_32_bits(H):
+    """A source, a matrix and a product of more than 2^31 elements: their last rows against the same
+    rows alone.  (More than 2^32 bytes: 4.6 GB each.)"""
+    R, C = 70016, 32768
+    assert R * C > 2 ** 31
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda")
+    for r in range(0, R, 8752):
+        x[r:r + 8752] = rand(r, 8752, C)
+    tail = slice(R - 200, R)
+    q = H.hinm_fp4_quantize(x, F.MX)
+    few = H.hinm_fp4_quantize(x[tail].contiguous(), F.MX)
+    assert torch.equal(q.values[-200 * C // 2:], few.values[:200 * C // 2])
+    y = H.hinm_fp4_dequantize(q)
+    assert torch.equal(y[tail], H.hinm_fp4_dequantize(few))
+    del q, y
+    q = H.hinm_fp4_quantize(x, F.NV, axis=0)       # the transpose: 32768 rows of depth 70016
+    y = H.hinm_fp4_dequantize(q, axis=0)
+    few = H.hinm_fp4_quantize(x[R - 256:].contiguous(), F.NV, axis=0)   # whole blocks of the depth
+    assert torch.equal(y[R - 256:], H.hinm_fp4_dequantize(few, axis=0))
+    del q, y, x
+    A, B, a, b = operands(H, 9, R, C, 128, F.MX)
+    Y = H.hinm_fp4_matmul(A, B)
+    check_product(Y[tail, -300:], a[tail], b[-300:])
+    check_product(Y[:100, :300], a[:100], b[:300])
+    H.hinm_fp4_matmul(B, A, Y_out=Y, transposed=True)    # the same products, by the other path
+    check_product(Y[tail, -300:], a[tail], b[-300:])
 
 
 # ----------------------------------------------------------------------------- products by expert
@@ -617,6 +718,48 @@ def test_another_stream(H):
     torch.cuda.synchronize()
     check_product(y1, a, b)
     check_product(y2, a, F.rounded(np64(x), F.NV, F.pow2_scale(np64(x))))
+
+
+def test_what_a_call_makes_belongs_to_its_stream(H):
+    """A call on a given stream while the current one is busy: its new tensors are filled on the stream
+    that writes them."""
+    o = [0, 30, 30, 60]
+    x, w = rand(1, 70, 256), rand(2, 3, 96, 256)
+    s = torch.cuda.Stream()
+    ragged = dict(ragged=H.HINM_RAGGED_ROWS, offsets=ints(o))
+    A = H.hinm_fp4_quantize(w, F.NV, tensor_scale="amax")
+    want = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", **ragged)
+    want_x = H.hinm_fp4_dequantize(want)
+    want_y = H.hinm_fp4_grouped_matmul(A, want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                  # some 10 ms of the current stream
+    q = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", stream=s, **ragged)
+    back = H.hinm_fp4_dequantize(q, stream=s)
+    y = H.hinm_fp4_grouped_matmul(A, q, stream=s)
+    assert not torch.cuda.current_stream().query()
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(q.tensor_scale, want.tensor_scale)
+    assert torch.equal(back, want_x) and torch.equal(y, want_y)
+
+
+def test_a_refused_call_leaves_the_matrix_as_it_was(H):
+    x = rand(1, 64, 256)
+    off = ints([0, 20, 64])
+    rag = dict(ragged=H.HINM_RAGGED_ROWS, offsets=off)
+    q = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", **rag)
+    want, g = H.hinm_fp4_dequantize(q), q.tensor_scale
+    bad = [dict(rag, tensor_scale=torch.ones(1, dtype=torch.float64, device="cuda")),
+           dict(rag, tensor_scale=torch.ones(1)), dict(rag, tensor_scale="max"),
+           dict(rag, offsets=off.long()), dict(rag, offsets=off.cpu()), dict(rag, offsets=ints([0, 64])),
+           dict(rag, offsets=None), dict(rag, ragged=H.HINM_RAGGED_DEPTH)]
+    for k in bad:
+        with pytest.raises(ValueError):
+            H.hinm_fp4_quantize(-x, F.NV, out=q, **k)
+    with pytest.raises(ValueError):
+        H.hinm_fp4_quantize(-x[:60], F.NV, out=q, **dict(rag, offsets=ints([0, 20, 60])))
+    assert q.offsets is off and q.tensor_scale is g
+    assert torch.equal(H.hinm_fp4_dequantize(q), want)
 
 
 def test_graph_replay(H):
