@@ -375,6 +375,15 @@ __device__ __forceinline__ uint32_t masked(uint32_t u, uint32_t bits2) {
   return u & m;
 }
 
+// The elements of 16 bytes whose bits are set.
+template <int DT>
+__device__ __forceinline__ uint4 masked_piece(const uint4& t, uint32_t k) {
+  if constexpr (DT == HINM_DTYPE_F32)
+    return make_uint4(k & 1u ? t.x : 0u, k & 2u ? t.y : 0u, k & 4u ? t.z : 0u, k & 8u ? t.w : 0u);
+  else
+    return make_uint4(masked(t.x, k), masked(t.y, k >> 2), masked(t.z, k >> 4), masked(t.w, k >> 6));
+}
+
 template <int DT, int FMT, bool VEC, bool RAGGED>
 __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a) {
   __shared__ ScaleTable table;
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
       if (row >= a.rows || real <= 0 || !placed[j0 + j]) continue;
       const T* p = src + (long long)row * a.ld;
       if (a.bits)
-        keep[j] = __ldg(a.bits + (batch * a.rows + row) * ((a.depth + 31) / 32) + k / 32) >> (k % 32);
+        keep[j] = __ldg(a.bits + (batch * a.rows + row) * ((a.depth + 31) / 32) + k / 32);
       p += k;
       // (rows that are not aligned: the aligned 16-byte pieces around the block, unless they reach
       // out of the matrix)
@@ -488,10 +497,13 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
       if (mine) {
         uint32_t w[B / 8];
         if (a.bits) {
+          // (shifted here: where it is loaded, the shift would wait for each row's word in turn;
+          // 11008 x 4096 bf16 NV 35.4 us, this way 28.4)
+          const uint32_t bits = keep[j] >> (k % 32);
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
-            if constexpr (k16) u[j][i] = masked(u[j][i], keep[j] >> (2 * i));
-            else u[j][i] = (keep[j] >> i) & 1u ? u[j][i] : 0u;
+            if constexpr (k16) u[j][i] = masked(u[j][i], bits >> (2 * i));
+            else u[j][i] = (bits >> i) & 1u ? u[j][i] : 0u;
           }
         }
         if constexpr (k16) {
@@ -593,9 +605,11 @@ __device__ __forceinline__ uint4 piece_anywhere(const T* p, uintptr_t lo, uintpt
 // sector.  A block of 32 lies in two neighbouring lanes.  (Two columns and 64 of the depth a thread,
 // with 4-byte loads, took 22.6 us at 4096 x 4096 bf16 NV and 33.6 us MX; this takes 11.2 and 8.9.)
 // ALIGNED: rows are aligned and of whole pieces.  (Six blocks an SM for fp32: 8192 x 8192 NV 50 us
-// instead of 58; bf16, whose blocks need their registers, 41.8 instead of 40.1.)
+// instead of 58, but with a mask's 16 bytes beside the elements 11008 x 4096 NV takes 73.8 us with
+// six, 44.0 with five; bf16, whose blocks need their registers, 41.8 instead of 40.1.)
 template <int DT, int FMT, bool MASK, bool ALIGNED>
-__global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? 6 : 1) quant_pieces_kernel(const QArgs a) {
+__global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 6) : 1)
+    quant_pieces_kernel(const QArgs a) {
   __shared__ ScaleTable table;
   fill<FMT>(table);
   ptx::enter_dependent();
@@ -618,28 +632,37 @@ __global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? 6 : 1) quant
   const uintptr_t lo = reinterpret_cast<uintptr_t>(src - c0);
   const uintptr_t hi = lo + ((unsigned long long)(a.depth - 1) * a.ld + a.rows) * sizeof(T);
   uint32_t u[16][4];
+  uint8_t keep[MASK ? 16 : 1];  // the byte of the mask that holds the piece's columns
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int d = part * 16 + i;
     uint4 t = make_uint4(0, 0, 0, 0);
+    if (MASK) keep[i] = 0;
     if (d < real) {
       const T* p = src + (long long)(k + d) * a.ld;
       if constexpr (ALIGNED) t = __ldg(reinterpret_cast<const uint4*>(p));
       else t = piece_anywhere(p, lo, hi);
-      if constexpr (MASK) {
-        const long long words = (a.rows + 31) / 32;
-        const uint32_t m = __ldg(a.bits + (batch * a.depth + k + d) * words + c0 / 32) >> (c0 % 32);
-        if constexpr (k16)
-          t = make_uint4(masked(t.x, m), masked(t.y, m >> 2), masked(t.z, m >> 4),
-                         masked(t.w, m >> 6));
-        else
-          t = make_uint4(m & 1u ? t.x : 0u, m & 2u ? t.y : 0u, m & 4u ? t.z : 0u, m & 8u ? t.w : 0u);
-      }
+      if constexpr (MASK)
+        keep[i] = __ldg(reinterpret_cast<const uint8_t*>(
+                            a.bits + (batch * a.depth + k + d) * ((a.rows + 31) / 32)) + c0 / 8);
     }
     u[i][0] = t.x;
     u[i][1] = t.y;
     u[i][2] = t.z;
     u[i][3] = t.w;
+  }
+  // (where a piece is loaded, its mask would make each load wait for the one before: 11008 x 4096
+  // bf16 NV 72.1 us, this way 37.7)
+  if constexpr (MASK) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 t = masked_piece<DT>(make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]),
+                                       (uint32_t)keep[i] >> (c0 % 8));
+      u[i][0] = t.x;
+      u[i][1] = t.y;
+      u[i][2] = t.z;
+      u[i][3] = t.w;
+    }
   }
   uint32_t am[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -997,14 +1020,6 @@ __device__ __forceinline__ uint32_t widest16(uint32_t m, const uint4& t) {
   }
   return m;
 }
-// The elements of 16 bytes whose bits are set.
-template <int DT>
-__device__ __forceinline__ uint4 masked_piece(const uint4& t, uint32_t k) {
-  if constexpr (DT == HINM_DTYPE_F32)
-    return make_uint4(k & 1u ? t.x : 0u, k & 2u ? t.y : 0u, k & 4u ? t.z : 0u, k & 8u ? t.w : 0u);
-  else
-    return make_uint4(masked(t.x, k), masked(t.y, k >> 2), masked(t.z, k >> 4), masked(t.w, k >> 6));
-}
 constexpr int kAhead = 4;  // pieces of 16 bytes that a thread loads before it uses the first
 
 template <int DT>
@@ -1048,12 +1063,13 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
         k[j] = 0;
         if (at < n) {
           t[j] = __ldg(p + at);
-          if (bits) k[j] = kPer == 8 ? __ldg(bits + at) : __ldg(bits + at / 2) >> (4 * (at & 1));
+          if (bits) k[j] = __ldg(bits + at * kPer / 8);
         }
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        m = widest16<DT, FINITE>(m, bits ? masked_piece<DT>(t[j], k[j]) : t[j]);
+        m = widest16<DT, FINITE>(
+            m, bits ? masked_piece<DT>(t[j], k[j] >> ((i + j * threads) * kPer % 8)) : t[j]);
     }
     return m;
   }
@@ -1064,23 +1080,27 @@ __device__ __forceinline__ uint32_t amax_share(const AmaxArgs& a, long long batc
   const long long total = (long long)(r1 - r0) * per;
   for (long long i = tid; i < total; i += kAhead * threads) {
     uint4 t[kAhead];
+    uint32_t k[kAhead];
+    int at_bit[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const long long at = i + j * threads;
       t[j] = make_uint4(0, 0, 0, 0);
+      k[j] = 0xFFFFFFFFu;
+      at_bit[j] = 0;
       if (at >= total) continue;
       const long long row = total < 0x7FFFFFFF ? (uint32_t)at / (uint32_t)per : at / per;
       const int unit = (int)(at - row * per);
       const int col = pieces ? unit * kPer : c0 + unit;
       const T* p = src + (r0 + row) * a.ld + col;
-      uint32_t k = 0xFFFFFFFFu;
-      if (a.bits)
-        k = __ldg(a.bits + (batch * a.rows + r0 + row) * words + col / 32) >> (col % 32);
-      if (pieces) t[j] = masked_piece<DT>(__ldg(reinterpret_cast<const uint4*>(p)), k);
-      else if (k & 1u) t[j].x = __ldg(p);
+      if (a.bits) k[j] = __ldg(a.bits + (batch * a.rows + r0 + row) * words + col / 32);
+      at_bit[j] = col % 32;
+      if (pieces) t[j] = __ldg(reinterpret_cast<const uint4*>(p));
+      else t[j].x = __ldg(p);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) m = widest16<DT, FINITE>(m, t[j]);
+    for (int j = 0; j < kAhead; ++j)
+      m = widest16<DT, FINITE>(m, a.bits ? masked_piece<DT>(t[j], k[j] >> at_bit[j]) : t[j]);
   }
   return m;
 }
