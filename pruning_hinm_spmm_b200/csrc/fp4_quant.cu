@@ -561,33 +561,25 @@ __global__ void __launch_bounds__(kQWarps * 32) quant_rows_kernel(const QArgs a)
 constexpr int kQDepth = 64;  // of the depth that a warp takes
 constexpr int kQThreads = 128;
 
-// The 16 bytes at p, which is aligned to its elements only: of 16-bit elements the one or two
-// aligned pieces around them (4883 x 3382 bf16 NV 17.9 us, element by element 25); of 32-bit ones,
-// or where the pieces reach out of [lo, hi), the elements inside it.
+// The 16 bytes at p, which is aligned to its elements only, in two steps, so that a thread's loads
+// need not wait for one another.  Of 16-bit elements: the one or two aligned pieces around them, and
+// then the bytes out of these; of 32-bit ones, or where the pieces reach out of [lo, hi): the
+// elements inside it.
+struct Around {
+  uint4 x, y;
+  int shift;  // bytes of x before the first element
+};
 template <class T>
-__device__ __forceinline__ uint4 piece_anywhere(const T* p, uintptr_t lo, uintptr_t hi) {
+__device__ __forceinline__ Around load_around(const T* p, uintptr_t lo, uintptr_t hi) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
-  const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-  uint32_t u[8];
-  if (sizeof(T) == 2 && at >= lo && at + (shift ? 32 : 16) <= hi) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-    const uint4 y = shift ? __ldg(reinterpret_cast<const uint4*>(at) + 1) : make_uint4(0, 0, 0, 0);
-    u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
-    u[4] = y.x, u[5] = y.y, u[6] = y.z, u[7] = y.w;
-    if (shift & 8) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
-    }
-    if (shift & 4) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
-    }
-    if (shift & 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
-    }
+  Around r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0),
+           (int)(reinterpret_cast<uintptr_t>(p) & 15)};
+  if (sizeof(T) == 2 && at >= lo && at + (r.shift ? 32 : 16) <= hi) {
+    r.x = __ldg(reinterpret_cast<const uint4*>(at));
+    if (r.shift) r.y = __ldg(reinterpret_cast<const uint4*>(at) + 1);
   } else {
-    u[0] = u[1] = u[2] = u[3] = 0;
+    r.shift = 0;
+    uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
       if (reinterpret_cast<uintptr_t>(p + i) + sizeof(T) <= hi) {
@@ -595,6 +587,23 @@ __device__ __forceinline__ uint4 piece_anywhere(const T* p, uintptr_t lo, uintpt
         else u[i] = __ldg(p + i);
       }
     }
+    r.x = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  return r;
+}
+__device__ __forceinline__ uint4 piece_of(const Around& r) {
+  uint32_t u[8] = {r.x.x, r.x.y, r.x.z, r.x.w, r.y.x, r.y.y, r.y.z, r.y.w};
+  if (r.shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
+  }
+  if (r.shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+  }
+  if (r.shift & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
@@ -633,23 +642,35 @@ __global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 
   const uintptr_t hi = lo + ((unsigned long long)(a.depth - 1) * a.ld + a.rows) * sizeof(T);
   uint32_t u[16][4];
   uint8_t keep[MASK ? 16 : 1];  // the byte of the mask that holds the piece's columns
+  // rows that a thread loads before it uses the first; rows that are not aligned bring two pieces
+  // each (3598 x 10954 bf16 NV, row by row 72.0 us, four at a time 38.8, eight 34.2; MX with a mask
+  // 74.9, 46.5 and 54.9)
+  constexpr int kRows = ALIGNED || !k16 ? 16 : MASK && FMT == HINM_FP4_MX ? 4 : 8;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int d = part * 16 + i;
-    uint4 t = make_uint4(0, 0, 0, 0);
-    if (MASK) keep[i] = 0;
-    if (d < real) {
-      const T* p = src + (long long)(k + d) * a.ld;
-      if constexpr (ALIGNED) t = __ldg(reinterpret_cast<const uint4*>(p));
-      else t = piece_anywhere(p, lo, hi);
-      if constexpr (MASK)
-        keep[i] = __ldg(reinterpret_cast<const uint8_t*>(
-                            a.bits + (batch * a.depth + k + d) * ((a.rows + 31) / 32)) + c0 / 8);
+  for (int i0 = 0; i0 < 16; i0 += kRows) {
+    Around t[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = i0 + j, d = part * 16 + i;
+      t[j] = Around{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), 0};
+      if (MASK) keep[i] = 0;
+      if (d < real) {
+        const T* p = src + (long long)(k + d) * a.ld;
+        if constexpr (ALIGNED) t[j].x = __ldg(reinterpret_cast<const uint4*>(p));
+        else t[j] = load_around(p, lo, hi);
+        if constexpr (MASK)
+          keep[i] = __ldg(reinterpret_cast<const uint8_t*>(
+                              a.bits + (batch * a.depth + k + d) * ((a.rows + 31) / 32)) + c0 / 8);
+      }
     }
-    u[i][0] = t.x;
-    u[i][1] = t.y;
-    u[i][2] = t.z;
-    u[i][3] = t.w;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const uint4 w = ALIGNED || !k16 ? t[j].x : piece_of(t[j]);
+      u[i0 + j][0] = w.x;
+      u[i0 + j][1] = w.y;
+      u[i0 + j][2] = w.z;
+      u[i0 + j][3] = w.w;
+    }
   }
   // (where a piece is loaded, its mask would make each load wait for the one before: 11008 x 4096
   // bf16 NV 72.1 us, this way 37.7)
