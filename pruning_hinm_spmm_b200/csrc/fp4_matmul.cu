@@ -18,10 +18,14 @@
 //   0      copies: per stage of 256 of the depth, TMA boxes of P and Q (128-byte rows, 128-byte
 //          swizzle) and the chunks of their scales
 //   1      MMA: scales to tensor memory, then up to four products a stage
-//   2..9   epilogue: 32 lanes of the accumulator and half of its columns each, 16 columns at a
-//          time in a loop that stays small (unrolled over a warp's columns it was bound by
-//          instruction fetches: one 256 x 256 tile with SiLU took 17.9 us), through a tile in
-//          shared memory, so that Y is written in whole 128-byte lines
+//   2..9   epilogue: 32 lanes of the accumulator and half of its columns each, 32 or 64 columns
+//          at a time, through a tile in shared memory, so that Y is written in whole 128-byte
+//          lines
+// What bounds it, measured at 4096 x 4096 x 16384 (pairs): NV takes 115.6 us, 109 without the
+// copies of the scales, 109 without the loads, 90 without both; MX 104.0, 103.7, 90.7, 83.5.  A
+// stage of 256 x 256 x 256 is 542 cycles of products at the nominal rate and takes 830 (NV) and
+// 740 (MX): the instructions that issue it, the 12 (6) scale copies among them, and 39 (36) KB a
+// stage into each SM's shared memory bind together.
 // The scales of a stage wait in a slot of tensor-memory columns, which is written again only
 // after the products that read it are done (the commit that frees their stage).  With few
 // tiles a cluster shares one tile's depth (SPLIT): each CTA leaves its partial sums in its own
@@ -366,7 +370,8 @@ __device__ __forceinline__ void stage_columns(const MmArgs& a, const Columns& c,
 
 // COLS columns that all count, of rows that are 32-byte aligned.  HOLD (one accumulator): all are
 // read first, and `done` is called, so that the accumulator is free while they are worked on (pairs
-// at 11008 x 4096 x 4096: 86.8 us, else 89.5).
+// at 11008 x 4096 x 4096: 86.8 us, else 89.5; with two accumulators it costs registers for nothing:
+// 4096 x 4096 x 1024 in 128 x 192 tiles 18.4 us, else 17.1).
 template <int DT, int COLS, bool BIASQ, bool HOLD, class Done>
 __device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool zero,
                                             const Columns& c, Done done) {
@@ -973,10 +978,11 @@ struct Plan {
 // the stages of a tile at the rate that the copies from L2 allow, and what a tile costs besides.
 // Measured on B200 (4096 x 4096, depths 256 to 16384; us a stage of 256 of the depth and us a tile
 // besides): pair 256 x 256 0.40 and 2.1, 128 x 192 0.465 and 0.95, 128 x 128 0.42 and 0.7, 128 x 64
-// 0.45 and 0.6; the last tile's columns are written after everything else, 0.011 a column.  So at depth 1024 128 x 192 takes 17.0 us and pairs 17.7, at 4096 45.0 and 35.9, at
-// 16384 156 and 115.  Sharing a tile's depth costs 1.5 us and 0.03 a column (partial sums through
-// the cluster): 4096 rows of depth 4096 by 1 column 7.1 us shared by four and 9.5 not, by 256
-// columns 13.1 shared by two and 10.4 not.
+// 0.45 and 0.6; the last tile's columns are written after everything else, 0.011 a column.  So at
+// depth 1024 128 x 192 takes 17.0 us and pairs 17.7, at 4096 45.0 and 35.9, at 16384 156 and 115.
+// Sharing a tile's depth costs 1.5 us and 0.03 a column (partial sums through the cluster): 4096
+// rows of depth 4096 by 1 column 7.1 us shared by four and 9.5 not, by 256 columns 13.1 shared by
+// two and 10.4 not.
 // p, q: rows of P and Q, in `groups` ragged parts when given (tokens: p_ragged or not).
 Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_groups, int times,
                int sms) {
