@@ -614,6 +614,13 @@ class Fp4Matrix:
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_c", (None, None))  # as_c() checks and builds again
 
+    def __getstate__(self):  # (copied and saved without the C struct, whose pointers are this one's)
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+
+    def __setstate__(self, state):
+        for k, v in state.items():
+            setattr(self, k, v)
+
     def as_c(self, device: Optional[int] = None) -> hinm_fp4:
         """The C struct of the buffers as they are now.  Checks that they are what it says; the
         struct is used again until a field is set or a tensor's memory moves."""

@@ -239,3 +239,15 @@ def test_binding_refuses_before_any_call(H):
         H._fp4_check_source(q, 1, 32, 5, 0)
     with pytest.raises(H.HinmError):
         H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 4, 0, "cpu")
+
+
+def test_matrices_are_copied_and_saved_without_their_c_struct(H):
+    import copy
+    import pickle
+    torch = pytest.importorskip("torch")
+    q = H.Fp4Matrix(format=H.HINM_FP4_MX, batch=1, rows=2, depth=128, values=torch.arange(128, dtype=torch.uint8),
+                    scales=torch.arange(512).to(torch.uint8))
+    object.__setattr__(q, "_c", ((0, 1, 2, None, None), H.hinm_fp4()))  # as after a call
+    for other in (copy.copy(q), copy.deepcopy(q), pickle.loads(pickle.dumps(q))):
+        assert other._c == (None, None) and other.rows == 2 and torch.equal(other.values, q.values)
+    assert q._c[0] is not None
