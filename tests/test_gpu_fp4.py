@@ -731,12 +731,13 @@ def test_what_a_call_makes_belongs_to_its_stream(H):
     want = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", **ragged)
     want_x = H.hinm_fp4_dequantize(want)
     want_y = H.hinm_fp4_grouped_matmul(A, want)
-    torch.cuda.synchronize()
-    torch.cuda._sleep(20_000_000)                  # some 10 ms of the current stream
-    q = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", stream=s, **ragged)
-    back = H.hinm_fp4_dequantize(q, stream=s)
-    y = H.hinm_fp4_grouped_matmul(A, q, stream=s)
-    assert not torch.cuda.current_stream().query()
+    for busy in (False, True):                     # (the first time, memory for the stream is found)
+        torch.cuda.synchronize()
+        if busy:
+            torch.cuda._sleep(20_000_000)          # some 10 ms of the current stream
+        q = H.hinm_fp4_quantize(x, F.NV, tensor_scale="amax", stream=s, **ragged)
+        back = H.hinm_fp4_dequantize(q, stream=s)
+        y = H.hinm_fp4_grouped_matmul(A, q, stream=s)
     s.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(q.tensor_scale, want.tensor_scale)
