@@ -613,11 +613,14 @@ __device__ __forceinline__ uint4 piece_of(const Around& r) {
 // of a row part are 128 contiguous bytes, and the 8 bytes that four lanes write for a column are one
 // sector.  A block of 32 lies in two neighbouring lanes.  (Two columns and 64 of the depth a thread,
 // with 4-byte loads, took 22.6 us at 4096 x 4096 bf16 NV and 33.6 us MX; this takes 11.2 and 8.9.)
-// ALIGNED: rows are aligned and of whole pieces.  (Six blocks an SM for fp32: 8192 x 8192 NV 50 us
-// instead of 58, but with a mask's 16 bytes beside the elements 11008 x 4096 NV takes 73.8 us with
-// six, 44.0 with five; bf16, whose blocks need their registers, 41.8 instead of 40.1.)
+// ALIGNED: rows are aligned and of whole pieces.
+// Blocks an SM, which bound a thread's registers: 16-bit elements five (11008 x 4096 bf16 NV 27.2 us,
+// with a mask 32.6; as many registers as are wanted, four and three blocks, 28.5 and 37.7; six would
+// spill), rows that start anywhere four (3598 x 10954 bf16 NV 34.1 us and 44.6, with five 36.9 and
+// 60.1); fp32 six (8192 x 8192 NV 50 us, else 58), but with a mask's 16 bytes beside the elements
+// five (11008 x 4096 NV 44.0 us, with six 73.8).
 template <int DT, int FMT, bool MASK, bool ALIGNED>
-__global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 6) : 1)
+__global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 6) : ALIGNED ? 5 : 4)
     quant_pieces_kernel(const QArgs a) {
   __shared__ ScaleTable table;
   fill<FMT>(table);
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 
     }
   }
   // (where a piece is loaded, its mask would make each load wait for the one before: 11008 x 4096
-  // bf16 NV 72.1 us, this way 37.7)
+  // bf16 NV 72.1 us, this way 37.7, in the blocks above 32.6)
   if constexpr (MASK) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -891,8 +894,10 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
 }
 
 // The way back for what quant_pieces_kernel takes: the same share of a thread.
+// (Five blocks an SM for MX: 8192 x 8192 bf16 37.6 us instead of 39.6; NV, whose table takes
+// registers, 46.9 instead of 37.5.)
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) dequant_pieces_kernel(const QArgs a) {
+__global__ void __launch_bounds__(kQThreads, FMT == HINM_FP4_MX ? 5 : 1) dequant_pieces_kernel(const QArgs a) {
   ptx::enter_dependent();
   if (a.early) ptx::launch_dependents();
   constexpr int B = fp4_block(FMT);
