@@ -621,6 +621,14 @@ class Fp4Matrix:
         for k, v in state.items():
             setattr(self, k, v)
 
+    def _changed(self, fields: dict) -> "Fp4Matrix":
+        """The same buffers with other fields."""
+        q = object.__new__(Fp4Matrix)
+        q.__dict__.update(self.__dict__)
+        for k, v in fields.items():
+            setattr(q, k, v)
+        return q
+
     def as_c(self, device: Optional[int] = None) -> hinm_fp4:
         """The C struct of the buffers as they are now.  Checks that they are what it says; the
         struct is used again until a field is set or a tensor's memory moves."""
@@ -736,7 +744,6 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
     ``stream``."""
     dev, s = _current(src, "src", stream)
     code, b, r, c, ld, bs = _matrix(src, "src")
-    # every check comes before the first change of `out`: a refused call leaves it as it was
     _fp4_check_mask(bitmask, b, r, c, dev)
     amax = isinstance(tensor_scale, str)
     if amax and tensor_scale != "amax":
@@ -745,6 +752,7 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
         raise ValueError("HINM_FP4_MX has no tensor scale")
     if ragged != HINM_RAGGED_NONE and offsets is None:
         raise ValueError("a ragged matrix needs offsets")
+    new = {}  # fields of `out` that this call exchanges
     if out is None:
         rows, depth = (r, c) if axis == 1 else (c, r)
         with _on(stream, dev):
@@ -755,28 +763,31 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
         if out.format != format or out.ragged != ragged:
             raise ValueError("out has another format or ragged form")
         _fp4_check_source(out, b, r, c, axis)
-        moved = ragged != HINM_RAGGED_NONE and out.offsets is not offsets
-        if moved:
+        if ragged != HINM_RAGGED_NONE and out.offsets is not offsets:
             if offsets.numel() != out.offsets.numel():
                 raise ValueError("offsets: need as many as out was made for")
-            _fp4_buffer(offsets, _torch().int32, 0, "offsets", dev)
-        if tensor_scale is not None and not amax and out.tensor_scale is not tensor_scale:
-            _fp4_buffer(tensor_scale, _torch().float32, b, "tensor_scale", dev)
-        if moved:
-            out.offsets = offsets
+            new["offsets"] = offsets
     if format == HINM_FP4_NV:
         if not amax:
             if out.tensor_scale is not tensor_scale:
-                out.tensor_scale = tensor_scale
+                new["tensor_scale"] = tensor_scale
         elif out.tensor_scale is None or out.given_scale:
             with _on(stream, dev):
-                out.tensor_scale = _torch().empty(b, dtype=_torch().float32, device=src.device)
+                new["tensor_scale"] = _torch().empty(b, dtype=_torch().float32, device=src.device)
         if out.given_scale == amax:
-            out.given_scale = not amax
-    cq, p, m = ctypes.byref(out.as_c(dev)), src.data_ptr(), _ptr(bitmask)
+            new["given_scale"] = not amax
+    # what changes goes into a copy of the description, which `out` takes over once the call has been
+    # accepted: a refused call, whichever side refuses it, leaves `out` as it was
+    q = out._changed(new) if new else out
+    as_c = q.as_c(dev)
+    cq, p, m = ctypes.byref(as_c), src.data_ptr(), _ptr(bitmask)
     if amax:
+        if ((as_c.values or 0) | (as_c.scales or 0)) & 15:  # (the scale's own call does not look at them)
+            raise ValueError("Fp4Matrix: need values and scales on 16-byte boundaries")
         _check(_lib.hinm_fp4_tensor_scale(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_tensor_scale")
     _check(_lib.hinm_fp4_quantize(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_quantize")
+    if new:
+        out.__dict__.update(q.__dict__)
     return out
 
 
