@@ -590,7 +590,10 @@ class Fp4Matrix:
     tensor_scale: object = None
     ragged: int = HINM_RAGGED_NONE
     offsets: object = None         # int32 [groups + 1] when ragged
-    given_scale: bool = False      # tensor_scale is the caller's: "amax" never writes into it
+    given_scale: bool = False      # tensor_scale is one that hinm_fp4_quantize was given
+    # the scale that this matrix made itself (allocate, "amax"): "amax" writes into no other.  Whatever the
+    # caller builds a matrix with or assigns, or a copy shares, is not it.
+    _made = None
 
     @property
     def groups(self) -> int:
@@ -604,18 +607,20 @@ class Fp4Matrix:
         torch = _torch()
         groups = 0 if ragged == HINM_RAGGED_NONE or offsets is None else offsets.numel() - 1
         v, s = hinm_fp4_size(format, batch, rows, depth, ragged, groups)
-        return cls(format=format, batch=batch, rows=rows, depth=depth,
-                   values=_empty_bytes(v, device), scales=_empty_bytes(s, device),
-                   tensor_scale=(torch.ones(batch, dtype=torch.float32, device=device)
-                                 if format == HINM_FP4_NV and tensor_scale else None),
-                   ragged=ragged, offsets=offsets)
+        q = cls(format=format, batch=batch, rows=rows, depth=depth,
+                values=_empty_bytes(v, device), scales=_empty_bytes(s, device),
+                tensor_scale=(torch.ones(batch, dtype=torch.float32, device=device)
+                              if format == HINM_FP4_NV and tensor_scale else None),
+                ragged=ragged, offsets=offsets)
+        q._made = q.tensor_scale
+        return q
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_c", (None, None))  # as_c() checks and builds again
 
     def __getstate__(self):  # (copied and saved without the C struct, whose pointers are this one's)
-        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_c", "_made")}
 
     def __setstate__(self, state):
         for k, v in state.items():
@@ -737,11 +742,13 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
     [b, ...] of them; the last dimension contiguous) in 4 bits, blocks along the depth.
 
     ``tensor_scale`` (HINM_FP4_NV): None (1), an fp32 tensor [batch] that is used (and kept) as it
-    is, or "amax": found on the device from src (hinm_fp4_tensor_scale).  ``bitmask``: hinm_mask's
-    words over src; elements whose bit is 0 count as 0.  ``ragged`` and ``offsets`` (int32
+    is, or "amax": found on the device from src (hinm_fp4_tensor_scale) and written into a tensor of
+    the matrix's own, never into one that the caller gave it (the next "amax" into the same matrix
+    writes that tensor again: another matrix that is to keep the scale takes a clone).  ``bitmask``:
+    hinm_mask's words over src; elements whose bit is 0 count as 0.  ``ragged`` and ``offsets`` (int32
     [groups + 1] on the device): tokens sorted by expert along the rows or along the depth.
-    ``out``: a matrix of the same sizes to write into.  What the call allocates itself belongs to
-    ``stream``."""
+    ``out``: a matrix of the same sizes to write into; a refused call leaves it as it was.  What the
+    call allocates itself belongs to ``stream``."""
     dev, s = _current(src, "src", stream)
     code, b, r, c, ld, bs = _matrix(src, "src")
     _fp4_check_mask(bitmask, b, r, c, dev)
@@ -771,9 +778,10 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
         if not amax:
             if out.tensor_scale is not tensor_scale:
                 new["tensor_scale"] = tensor_scale
-        elif out.tensor_scale is None or out.given_scale:
+        elif out._made is None or out.tensor_scale is not out._made or out.given_scale:
             with _on(stream, dev):
-                new["tensor_scale"] = _torch().empty(b, dtype=_torch().float32, device=src.device)
+                new["_made"] = _torch().empty(b, dtype=_torch().float32, device=src.device)
+            new["tensor_scale"] = new["_made"]
         if out.given_scale == amax:
             new["given_scale"] = not amax
     # what changes goes into a copy of the description, which `out` takes over once the call has been

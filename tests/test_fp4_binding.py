@@ -85,3 +85,44 @@ def test_an_accepted_call_takes_the_new_offsets_and_scale(H, monkeypatch):
     at = [t.data_ptr() for t in (mine, off, g, off2)]
     assert noted.calls == [("hinm_fp4_tensor_scale", at[0], at[1]), ("hinm_fp4_quantize", at[0], at[1]),
                            ("hinm_fp4_quantize", at[2], at[3]), ("hinm_fp4_quantize", None, at[3])]
+
+
+def test_amax_never_writes_into_a_scale_that_the_caller_gave(H, monkeypatch):
+    """However the matrix came by it: "amax" takes a tensor of its own, once, and leaves the caller's."""
+    import copy
+    import dataclasses
+    import pickle
+    noted = Noted(H._lib, "hinm_fp4_tensor_scale", "hinm_fp4_quantize")
+    monkeypatch.setattr(H, "_lib", noted)
+    x = torch.zeros(64, 256, dtype=BF16)
+    amax = lambda q: H.hinm_fp4_quantize(x, H.HINM_FP4_NV, tensor_scale="amax", out=q)  # noqa: E731
+    g = torch.full((1,), 0.5)
+    built = H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 64, 256, "cpu", tensor_scale=False)
+    ways = {
+        "constructor": H.Fp4Matrix(format=H.HINM_FP4_NV, batch=1, rows=64, depth=256, values=built.values,
+                                   scales=built.scales, tensor_scale=g),
+        "assigned": H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 64, 256, "cpu"),
+        "assigned to amax's": amax(H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 64, 256, "cpu")),
+        "quantised with": H.hinm_fp4_quantize(x, H.HINM_FP4_NV, tensor_scale=g),
+    }
+    ways["assigned"].tensor_scale = g
+    ways["assigned to amax's"].tensor_scale = g
+    first = amax(H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 64, 256, "cpu"))
+    theirs = first.tensor_scale          # the scale of another matrix, taken over by its copies
+    copies = {"replace": dataclasses.replace(first, values=first.values.clone()), "copy": copy.copy(first)}
+    for name, q in {**ways, **copies}.items():
+        kept = g if name in ways else theirs
+        assert q.tensor_scale is kept, name
+        amax(q)
+        made = q.tensor_scale
+        assert made is not kept and not q.given_scale, name
+        assert noted.calls[-2:] == [(f, made.data_ptr(), None) for f in
+                                    ("hinm_fp4_tensor_scale", "hinm_fp4_quantize")], name
+        amax(q)
+        assert q.tensor_scale is made, name  # its own is written again, where it is
+    for q in (copy.deepcopy(first), pickle.loads(pickle.dumps(first))):
+        amax(q)
+        assert q.tensor_scale is not theirs
+    own = H.Fp4Matrix.allocate(H.HINM_FP4_NV, 1, 64, 256, "cpu")
+    ones = own.tensor_scale
+    assert amax(own).tensor_scale is ones    # (allocate's ones are the matrix's own)
