@@ -438,10 +438,11 @@ hinm_status hinm_spmm_epilogue(const hinm_layout* layout, const void* X, int N, 
  *            Rows past the last are not written.
  * Ragged matrices hold tokens sorted by group (expert), group e's at [offsets[e], offsets[e+1])
  * of the token dimension, which has `rows` (HINM_RAGGED_ROWS) or `depth` (HINM_RAGGED_DEPTH)
- * places in all; tokens before the first or behind the last group are neither read nor
- * written.  offsets: device int32 [groups + 1], nondecreasing, inside the dimension; offsets
- * that are not set HINM_ERR_INVALID_ARG in the device status word, and nothing outside the
- * matrices is read or written.
+ * places in all; tokens before the first or behind the last group count for nothing and their
+ * places are not written.  offsets: device int32 [groups + 1], nondecreasing, inside the
+ * dimension; every call that is given others sets HINM_ERR_INVALID_ARG in the device status
+ * word, reads and writes nothing outside the matrices, and leaves what it writes unspecified
+ * (the products write nothing).
  *   ragged rows:  values as above; group e's scale tiles start at tile offsets[e] / 128 + e
  *                 (rows / 128 + groups tiles, division rounded down)
  *   ragged depth: D = 128 (depth / 128 + groups); group e's tokens start at stored depth

@@ -935,8 +935,10 @@ hinm_status hinm_fp4_tensor_scale(const void* src, int dtype, long long ld, long
     st = check_fp4_source(src, dtype, ld, batch_stride, axis, bitmask, q, "src");
     if (st != HINM_OK) return st;
   }
+  int* status = hinm::device_status_ptr();
+  if (!status) return fail(HINM_ERR_CUDA, "no device status word");
   cudaError_t e = hinm::launch_fp4_tensor_scale(src, dtype, ld, batch_stride, axis, bitmask, *q,
-                                                static_cast<cudaStream_t>(stream));
+                                                status, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "hinm_fp4_tensor_scale launch");
   return ok();
 }

@@ -158,7 +158,7 @@ cudaError_t launch_spmm(const hinm_layout& L, const uint16_t* X, int N, const Sp
 // Microscaled 4-bit matrices (arguments checked by the caller).
 cudaError_t launch_fp4_tensor_scale(const void* src, int dtype, long long ld,
                                     long long batch_stride, int axis, const uint32_t* bits,
-                                    const hinm_fp4& q, cudaStream_t s);
+                                    const hinm_fp4& q, int* status, cudaStream_t s);
 cudaError_t launch_fp4_quantize(const void* src, int dtype, long long ld, long long batch_stride,
                                 int axis, const uint32_t* bits, const hinm_fp4& q, int* status,
                                 cudaStream_t s);
