@@ -27,6 +27,10 @@
 namespace hinm {
 namespace {
 
+using ptx::F2;
+using ptx::fma2;
+using ptx::mul2;
+
 // ------------------------------------------------------------------ elements
 template <int DT>
 struct Elem;
@@ -54,23 +58,6 @@ struct Elem<HINM_DTYPE_F32> {
   static __device__ T of(float v) { return __float_as_uint(v); }
 };
 
-// Two fp32 values in one register pair, for the packed fp32 instructions.
-struct F2 {
-  unsigned long long v;
-  __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ explicit F2(unsigned long long u) : v(u) {}
-  __device__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return F2(r);
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return F2(r);
-}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -64,6 +64,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 2^x, 2 units in the last place off; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 1 / x, 1 unit in the last place off; results below 2^-126 are 0.
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---------------------------------------------------------------- packed fp32
+// Two fp32 values in one register pair, for the packed fp32 instructions.
+struct F2 {
+  unsigned long long v;
+  __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ explicit F2(unsigned long long u) : v(u) {}
+  __device__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return F2(r);
+}
+
 // ---------------------------------------------------------------- cp.async (16-, 8-, 4-byte)
 // dst: shared-memory address, src: global; both aligned to the size.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

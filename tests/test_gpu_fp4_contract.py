@@ -66,3 +66,60 @@ def test_every_call_reports_bad_offsets_by_itself(H, fmt, axis, ragged, o, bad, 
     assert H.hinm_device_status() == want
     H.hinm_fp4_dequantize(q, axis=axis, out=wide)
     assert H.hinm_device_status() == want
+
+
+# ----------------------------------------------------------------------------- activations
+def silu64(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z < 0, z * e, z) / (1 + e)
+
+
+def arguments():
+    """Both tails to where the result is 0 or the argument, both sides of 0 from the smallest number on."""
+    line = np.linspace(-115.0, 115.0, 5000)
+    small = np.logspace(-45, 38.5, 900)
+    z = np.concatenate([line, np.linspace(-16, 3, 2000), small, -small, [0.0, -0.0, 3.4e38, -3.4e38]])
+    return z.astype(np.float32)
+
+
+def of_bias(H, z, dtype, act, N, K, transposed):
+    """act(z) for each z, as the bias of a product of zeros: [len(z)] rows of N equal columns."""
+    M = len(z)
+    A = H.hinm_fp4_quantize(torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), F.MX)
+    B = H.hinm_fp4_quantize(rand(1, N, K), F.MX)
+    y = H.hinm_fp4_matmul(A, B, dtype=dtype, transposed=transposed, bias=torch.from_numpy(z).cuda(), activation=act)
+    y = y.t() if transposed else y
+    assert ((y == y[:, :1]) | (y.isnan() & y[:, :1].isnan())).all()
+    return y[:, 0].double().cpu().numpy()
+
+
+def check_tails(got, want, dtype, own):
+    """own: the activation's own error relative to the value.  Besides it the store rounds by half a step,
+    relative where the value is normal in dtype and of the smallest subnormal where it is not; 2^-140 stands
+    for what goes under in fp32 on the way.  What is at least half a step past dtype's largest number is
+    infinite: that number is (2 - eps) 2^e, steps there are eps 2^e, so the border is (2 - eps / 2) 2^e (fp16:
+    65520)."""
+    info = torch.finfo(dtype)
+    store = 0.0 if dtype == torch.float32 else info.eps / 2
+    over = np.abs(want) >= (2 - info.eps / 2) * 2.0 ** np.floor(np.log2(info.max))
+    assert np.array_equal(np.isinf(got), over)
+    err = np.abs(want) * (own + store * (1 + own)) + 2.0 ** -140 + info.tiny * info.eps / 2
+    bad = ~over & ~(np.abs(got - want) <= err)
+    assert not bad.any(), (int(bad.sum()), want[bad][:5], got[bad][:5])
+
+
+# (rows x columns: the accumulator's rows along Y's rows, along its columns, tokens in the lanes; shared depth)
+LAYOUTS = pytest.mark.parametrize("N,K,transposed,M", [(1, 32, False, None), (70, 32, False, None), (5, 32, True, None),
+                                                       (100, 32, True, None), (2, 4096, False, 640), (2, 4096, True, 640)])
+DTYPES = pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])
+
+
+@DTYPES
+@LAYOUTS
+def test_silu_in_both_tails(H, dtype, N, K, transposed, M):
+    z = arguments()[::1 if M is None else 13][:M]
+    own = 2.0 ** -20 if dtype == torch.float32 else 2.0 ** -16
+    z64 = z.astype(np.float64)
+    check_tails(of_bias(H, z, dtype, H.HINM_ACT_SILU, N, K, transposed), silu64(z64), dtype, own)
+    ends = of_bias(H, np.array([np.inf, np.nan], np.float32), dtype, H.HINM_ACT_SILU, N, K, transposed)
+    assert ends[0] == np.inf and np.isnan(ends[1])
