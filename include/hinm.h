@@ -504,7 +504,8 @@ hinm_status hinm_fp4_dequantize(const hinm_fp4* q, int axis, void* dst, int dtyp
  *   Y[m][n] = act(gA gB sum_k A[m][k] B[n][k] + bias[m])
  * summed in fp32 on the tensor cores over codes and block scales, times gA gB (itself rounded
  * to fp32), rounded once to Y's type.  SiLU(z) is within 2^-20 |SiLU(z)| + 2^-140 of its value
- * (16-bit Y: within 2^-16 |SiLU(z)| + 2^-140 before the rounding to Y's type), ReLU keeps NaN.
+ * (16-bit Y: within 2^-16 |SiLU(z)| + 2^-140 before the rounding to Y's type), GELU(z) =
+ * z erfc(-z / sqrt 2) / 2 within (z^2 + 16) 2^-23 |GELU(z)| + 2^-140; ReLU keeps NaN.
  * A: rows M (a weight's output channels), B: rows N (tokens), the same depth, neither ragged,
  * batch 1.  Y_out: dtype HINM_DTYPE_*, [M][N] with ldy >= N elements from row to row, or
  * (transposed) [N][M] with ldy >= M; aligned to its element.  bias: device fp32 [M] or NULL.

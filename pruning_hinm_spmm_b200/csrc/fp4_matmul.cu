@@ -228,6 +228,29 @@ __device__ __forceinline__ float silu_quick(float x) {
   constexpr float k16 = 1.52587890625e-5f;  // 2^-16
   return x * (ptx::rcp(ptx::ex2(fmaf(x, -1.4426950408889634f, -16.0f)) + k16) * k16);
 }
+// GELU(x) = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 = e^(-a^2/2) w(t), t = 1 / (1 + 0.3 a): without a
+// difference of nearly equal numbers for either sign (1 + erf(x / sqrt 2) has none of its digits right
+// from -5.6 on).  An exponential times a polynomial in t is the form of Hastings (Approximations for
+// Digital Computers, 1955); the coefficients are a fit of their own, in relative error over a <= 14.5 (2^-24;
+// 2^-21 as evaluated in fp32).  The exponential is the square of h = 2^(-a^2 log2(e) / 4), which is
+// normal as long as GELU(x) is; its argument's roundings make the error (z^2 + 16) 2^-23 of GELU(z), as
+// large as one half step of z does.  (11008 x 4096 x 4096 bf16 105.5 us, with erff 119, with erfcf 256.)
+__device__ __forceinline__ float gelu(float x) {
+  const float a = fabsf(x);
+  const float t = ptx::rcp(fmaf(a, 0.3f, 1.0f));
+  float w = 0.03840738907456398f;
+  w = fmaf(w, t, -0.16930744051933289f);
+  w = fmaf(w, t, 0.22895173728466034f);
+  w = fmaf(w, t, -0.07683960348367691f);
+  w = fmaf(w, t, 0.14276523888111115f);
+  w = fmaf(w, t, 0.09458588063716888f);
+  w = fmaf(w, t, 0.12194526195526123f);
+  w = fmaf(w, t, 0.11948420852422714f);
+  w = fmaf(w, t, 7.3723608693399e-06f);
+  const float h = ptx::ex2(a * a * -0.36067376022224085f);
+  const float q = (w * h) * h;
+  return x * (x < 0.0f ? q : 1.0f - q);
+}
 // PRECISE: for outputs in 32 bits.
 template <int ACT, bool PRECISE>
 __device__ __forceinline__ float activate(float x) {
@@ -235,7 +258,7 @@ __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == HINM_ACT_SILU) {
     return PRECISE ? silu(x) : silu_quick(x);
   }
-  if constexpr (ACT == HINM_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+  if constexpr (ACT == HINM_ACT_GELU) return gelu(x);
   return x;
 }
 template <bool PRECISE>

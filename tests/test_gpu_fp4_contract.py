@@ -123,3 +123,21 @@ def test_silu_in_both_tails(H, dtype, N, K, transposed, M):
     check_tails(of_bias(H, z, dtype, H.HINM_ACT_SILU, N, K, transposed), silu64(z64), dtype, own)
     ends = of_bias(H, np.array([np.inf, np.nan], np.float32), dtype, H.HINM_ACT_SILU, N, K, transposed)
     assert ends[0] == np.inf and np.isnan(ends[1])
+
+
+def gelu64(z):
+    """z Phi(z) with Phi's small side as erfc: 1 + erf would have lost it."""
+    from math import erfc
+    small = np.array([0.5 * erfc(abs(float(v)) * np.sqrt(0.5)) for v in z])
+    return z * np.where(z < 0, small, 1 - small)
+
+
+@DTYPES
+@LAYOUTS
+def test_gelu_in_both_tails(H, dtype, N, K, transposed, M):
+    z = arguments()[::1 if M is None else 13][:M]
+    z64 = z.astype(np.float64)
+    own = (np.minimum(z64 * z64, 240.0) + 16) * 2.0 ** -23   # (past 15.4 GELU is 0 or z itself)
+    check_tails(of_bias(H, z, dtype, H.HINM_ACT_GELU, N, K, transposed), gelu64(z64), dtype, own)
+    ends = of_bias(H, np.array([np.inf, np.nan], np.float32), dtype, H.HINM_ACT_GELU, N, K, transposed)
+    assert ends[0] == np.inf and np.isnan(ends[1])
