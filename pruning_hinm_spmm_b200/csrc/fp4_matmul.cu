@@ -206,7 +206,8 @@ __device__ __forceinline__ float silu(float x) {
   return x * (ptx::rcp(fmaf(h * kTwo32, h, kTwo32)) * kTwo32);
 }
 // Two at once, in packed instructions: 4096 x 4096 x 512 25.8 us, one by one 30.5.  (Where the columns are
-// held in registers, the pairs' kernel, it would spill: 11008 x 4096 x 4096 105 us, one by one 98.5.)
+// held in registers, the pairs' kernel, they cost more than they save: 11008 x 4096 x 4096 105 us, one by
+// one 101, with the quick exponential 95.)
 __device__ __forceinline__ void silu2(float& xa, float& xb) {
   using ptx::F2;
   const F2 y(fminf(xa, 128.0f), fminf(xb, 128.0f));
@@ -784,6 +785,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       if (ptx::elect_one()) commit<PAIR>(accf_bar(b));
       __syncwarp();
     }
+    // Rank 1 of a pair issues nothing: it comes to the drain at once, and a wait there would last, and
+    // be limited, for the whole kernel.  The epilogue's waits span a tile each, and behind its last tile
+    // only the drain's own commit is left.
+    if (PAIR && rank != 0) asm volatile("barrier.cta.sync 2, %0;" ::"n"(32 + 32 * kEpiWarps) : "memory");
     if (ptx::elect_one()) {
       if (!PAIR || rank == 0) commit<PAIR>(drain_bar);  // the last commit that reaches rank 1
       ptx::mbar_wait(drain_bar, 0, a.status, nullptr);
@@ -897,6 +902,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       }
       if (col0 >= col1) release(b);  // none of the columns
     }
+    if (PAIR && rank != 0) asm volatile("barrier.cta.arrive 2, %0;" ::"n"(32 + 32 * kEpiWarps) : "memory");
   }
   if constexpr (SPLIT) {
     ptx::cluster_sync();  // every CTA's partial sums are in its shared memory

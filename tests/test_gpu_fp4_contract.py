@@ -141,3 +141,29 @@ def test_gelu_in_both_tails(H, dtype, N, K, transposed, M):
     check_tails(of_bias(H, z, dtype, H.HINM_ACT_GELU, N, K, transposed), gelu64(z64), dtype, own)
     ends = of_bias(H, np.array([np.inf, np.nan], np.float32), dtype, H.HINM_ACT_GELU, N, K, transposed)
     assert ends[0] == np.inf and np.isnan(ends[1])
+
+
+# ----------------------------------------------------------------------------- waits
+def test_a_product_that_lasts_longer_than_a_wait_may(H):
+    """Waits inside the kernels are limited to 2 s each.  A product of 1.9e16 operations takes longer than that
+    (2.1 s at the tensor cores' nominal rate), by tiles of 10 ms: right, and no wait ran out.  Every code is 1
+    with the scale 1, so that every output is the depth."""
+    M, K = 61440, 2_500_096
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 100 GB")
+    A = H.Fp4Matrix.allocate(F.MX, 1, M, K, "cuda")
+    A.values.fill_(0x22)
+    A.scales.fill_(127)
+    Y = torch.empty(M, M, device="cuda")
+    assert H.hinm_device_status() == 0
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    H.hinm_fp4_matmul(A, A, Y_out=Y)
+    end.record()
+    torch.cuda.synchronize()
+    assert H.hinm_device_status() == 0
+    assert start.elapsed_time(end) > 2000
+    assert float(Y.min()) == K and float(Y.max()) == K
+    del A, Y
+    torch.cuda.empty_cache()
