@@ -541,6 +541,15 @@ hinm_status hinm_fp4_grouped_weight_grad(const hinm_fp4* A, const hinm_fp4* B, v
  * Read the result with hinm_device_status(); the context stays usable. */
 hinm_status hinm_selftest_wait_timeout(unsigned long long limit_ns, void* stream);
 
+/* Diagnostic: how the 4-bit product of A and B (hinm_fp4_matmul, or by expert when B is ragged) is
+ * cut, which depends on the two shapes alone; offsets and buffers are not looked at, nothing is
+ * launched.  cut_host[4]: columns of a tile (64, 128, 192 or 256); 1 when a pair of CTAs takes it;
+ * CTAs that share a tile's depth; 1 when the tokens are the accumulator's lanes.  Zeros when there
+ * is nothing to multiply.  For the number of SMs of the current device (148 without one).
+ * Errors: HINM_ERR_SHAPE, HINM_ERR_INVALID_ARG, HINM_ERR_UNSUPPORTED. */
+hinm_status hinm_selftest_fp4_cut(const hinm_fp4* A, const hinm_fp4* B, int transposed,
+                                  int32_t* cut_host);
+
 /* Reads the device status word into *status_host (0 = no fault; else an hinm_status)
  * and clears it.  Synchronises `stream`. */
 hinm_status hinm_device_status(void* stream, int32_t* status_host);

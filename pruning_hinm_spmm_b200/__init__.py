@@ -122,6 +122,7 @@ _SIGS = {
     "hinm_fp4_matmul": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i32, _vp, _i32, _vp]),
     "hinm_fp4_grouped_matmul": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i32, _vp, _i32, _vp]),
     "hinm_fp4_grouped_weight_grad": (_i32, [_fp4p, _fp4p, _vp, _i32, _i64, _i64, _vp]),
+    "hinm_selftest_fp4_cut": (_i32, [_fp4p, _fp4p, _i32, ctypes.POINTER(ctypes.c_int32)]),
     "hinm_device_status": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32)]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -884,6 +885,17 @@ def hinm_fp4_grouped_weight_grad(A: Fp4Matrix, B: Fp4Matrix, Y_out=None, dtype=N
                                              Y_out.data_ptr(), code, ldy, bs, s),
            "hinm_fp4_grouped_weight_grad")
     return Y_out
+
+
+def hinm_selftest_fp4_cut(A: Fp4Matrix, B: Fp4Matrix, transposed: bool = False) -> Tuple[int, int, int, int]:
+    """How the product of A and B is cut (their buffers are not looked at and may be None): columns of
+    a tile, 1 for pairs of CTAs, CTAs that share a tile's depth, 1 when the tokens are the lanes."""
+    c = [hinm_fp4(HINM_FP4_LAYOUT_VERSION, q.format, q.batch, q.rows, q.depth, q.ragged, q.groups)
+         for q in (A, B)]
+    cut = (ctypes.c_int32 * 4)()
+    _check(_lib.hinm_selftest_fp4_cut(ctypes.byref(c[0]), ctypes.byref(c[1]), 1 if transposed else 0,
+                                      cut), "hinm_selftest_fp4_cut")
+    return tuple(cut)
 
 
 def hinm_device_status(stream=None) -> int:

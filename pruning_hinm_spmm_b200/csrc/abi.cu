@@ -1028,6 +1028,30 @@ hinm_status hinm_fp4_grouped_weight_grad(const hinm_fp4* A, const hinm_fp4* B, v
                      stream, "hinm_fp4_grouped_weight_grad launch");
 }
 
+hinm_status hinm_selftest_fp4_cut(const hinm_fp4* A, const hinm_fp4* B, int transposed,
+                                  int32_t* cut_host) {
+  if (!A || !B || !cut_host) return fail(HINM_ERR_INVALID_ARG, "A, B or cut_host is NULL");
+  for (const hinm_fp4* q : {A, B}) {
+    hinm_status st =
+        check_fp4_shape(q->format, q->batch, q->rows, q->depth, q->ragged, q->groups);
+    if (st != HINM_OK) return st;
+  }
+  if (A->format != B->format || A->depth != B->depth)
+    return fail(HINM_ERR_SHAPE, "A and B have different formats or depths");
+  const bool by_depth = B->ragged == HINM_RAGGED_DEPTH;
+  if (A->ragged != (by_depth ? HINM_RAGGED_DEPTH : HINM_RAGGED_NONE) ||
+      (by_depth ? A->groups != B->groups
+                : A->batch != (B->ragged == HINM_RAGGED_ROWS ? B->groups : B->batch)))
+    return fail(HINM_ERR_UNSUPPORTED, "no product takes these matrices together");
+  hinm::Fp4Cut c{};
+  if (B->rows > 0) c = hinm::fp4_cut(*A, *B, transposed != 0);
+  cut_host[0] = c.columns;
+  cut_host[1] = c.pair;
+  cut_host[2] = c.split;
+  cut_host[3] = c.tokens_in_lanes;
+  return ok();
+}
+
 hinm_status hinm_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {
   if (limit_ns == 0 || limit_ns > 2000000000ull)
     return fail(HINM_ERR_INVALID_ARG, "limit_ns=%llu: need 0 < limit_ns <= 2e9", limit_ns);

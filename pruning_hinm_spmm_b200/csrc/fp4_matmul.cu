@@ -1087,6 +1087,23 @@ Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_gr
   return best;
 }
 
+// Which side takes the accumulator's lanes, and the cut: both of the shapes alone.
+struct Choice {
+  bool swap;  // the tokens in the lanes
+  Plan plan;
+};
+Choice choose(const hinm_fp4& A, const hinm_fp4& B, bool transposed) {
+  const bool by_rows = B.ragged == HINM_RAGGED_ROWS, by_depth = B.ragged == HINM_RAGGED_DEPTH;
+  const int n = by_rows ? (B.rows + B.groups - 1) / B.groups : B.rows;
+  Choice c;
+  c.swap = transposed && n > 64;
+  const int groups = by_rows ? B.groups : 0;
+  c.plan = make_plan(c.swap ? B.rows : A.rows, c.swap ? A.rows : B.rows,
+                     by_depth ? B.depth / B.groups : B.depth, c.swap ? groups : 0,
+                     c.swap ? 0 : groups, by_depth ? B.groups : 1, num_sms());
+  return c;
+}
+
 template <int FMT, int BN, bool PAIR>
 cudaError_t launch_tiles(MmArgs a, const Maps& m, const Plan& p, cudaStream_t s) {
   constexpr int PR = MmCfg<FMT, BN, PAIR>::kPRows;
@@ -1117,17 +1134,13 @@ cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed
   const Side sb{B.scales, (int)gb.row_tiles, (int)gb.chunks(FMT), B.rows, 0,
                 a.ragged == HINM_RAGGED_ROWS ? 1 : 0};
   a.steps = (int)(ga.depth_pad / 64);
-  const int n = a.ragged == HINM_RAGGED_ROWS ? (B.rows + a.groups - 1) / a.groups : B.rows;
-  const bool swap = transposed && n > 64;  // tokens in the lanes
+  const Choice choice = choose(A, B, transposed);
+  const bool swap = choice.swap;
+  const Plan p = choice.plan;
   a.p = swap ? sb : sa;
   a.q = swap ? sa : sb;
   a.bias_q = swap;
   a.q_major = transposed && !swap;
-  const int g = a.ragged == HINM_RAGGED_ROWS ? a.groups : 0;
-  Plan p = make_plan(a.p.rows, a.q.rows,
-                     a.ragged == HINM_RAGGED_DEPTH ? a.depth / a.groups : a.depth,
-                     a.p.ragged ? g : 0, a.q.ragged ? g : 0,
-                     a.ragged == HINM_RAGGED_DEPTH ? a.groups : 1, num_sms());
   Maps m{};
   const int q_box = p.pair ? p.bn / 2 : p.bn == 64 ? 16 : 64;  // MmCfg::kQBox
   if (!make_map(swap ? &m.q : &m.p, A.values, (long long)A.batch * A.rows, ga.pitch(),
@@ -1147,6 +1160,11 @@ cudaError_t pick(MmArgs a, const hinm_fp4& A, const hinm_fp4& B, bool transposed
 }
 
 }  // namespace
+
+Fp4Cut fp4_cut(const hinm_fp4& A, const hinm_fp4& B, bool transposed) {
+  const Choice c = choose(A, B, transposed);
+  return Fp4Cut{c.plan.bn, c.plan.pair, c.plan.split, c.swap ? 1 : 0};
+}
 
 cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out& o, int* status,
                               cudaStream_t s) {

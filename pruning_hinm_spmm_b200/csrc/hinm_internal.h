@@ -176,6 +176,11 @@ struct Fp4Out {
 };
 cudaError_t launch_fp4_matmul(const hinm_fp4& A, const hinm_fp4& B, const Fp4Out& o, int* status,
                               cudaStream_t s);
+// How it cuts the product (hinm_selftest_fp4_cut).
+struct Fp4Cut {
+  int columns, pair, split, tokens_in_lanes;
+};
+Fp4Cut fp4_cut(const hinm_fp4& A, const hinm_fp4& B, bool transposed);
 
 // Shared by the rank users (search and mask): V (fp64 column sums per tile) and the rank
 // of every working position.

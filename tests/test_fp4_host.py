@@ -251,3 +251,30 @@ def test_matrices_are_copied_and_saved_without_their_c_struct(H):
     for other in (copy.copy(q), copy.deepcopy(q), pickle.loads(pickle.dumps(q))):
         assert other._c == (None, None) and other.rows == 2 and torch.equal(other.values, q.values)
     assert q._c[0] is not None
+
+
+# ----------------------------------------------------------------------------- cuts of a product
+def test_every_cut_is_reached_by_some_size(H):
+    """The sizes that the GPU tests take for each kernel of the product exist."""
+    import fp4_cuts
+    missing = [c for c in fp4_cuts.CUTS if fp4_cuts.find(H, *c) is None]
+    assert not missing, missing
+
+
+def test_cut_of_a_product(H):
+    import fp4_cuts
+    cut = lambda *a: fp4_cuts.cut(H, *a)  # noqa: E731
+    assert cut("plain", 11008, 4096, 4096, 1, False) == (256, 1, 1, 0)
+    assert cut("plain", 4096, 1, 4096, 1, True)[::2] == (64, 4)
+    assert cut("plain", 300, 64, 300, 1, True)[3] == 0 and cut("plain", 300, 65, 300, 1, True)[3] == 1
+    assert cut("rows", 300, 0, 300, 4, True) == (0, 0, 0, 0)          # no tokens: nothing to multiply
+    L, out = H.lib(), (ctypes.c_int32 * 4)()
+    call = lambda a, b, o=out: L.hinm_selftest_fp4_cut(ctypes.byref(a), ctypes.byref(b), 0, o)  # noqa: E731
+    assert call(_fp4(H), _fp4(H)) == H.HINM_OK and out[0] == 64
+    assert call(_fp4(H, rows=0), _fp4(H)) == H.HINM_ERR_SHAPE
+    assert call(_fp4(H), _fp4(H, depth=256)) == H.HINM_ERR_SHAPE
+    assert call(_fp4(H), _fp4(H, batch=2)) == H.HINM_ERR_UNSUPPORTED
+    assert call(_fp4(H, ragged=1, groups=2), _fp4(H, ragged=1, groups=2)) == H.HINM_ERR_UNSUPPORTED
+    assert call(_fp4(H, batch=3), _fp4(H, ragged=1, groups=2)) == H.HINM_ERR_UNSUPPORTED
+    assert L.hinm_selftest_fp4_cut(None, None, 0, out) == H.HINM_ERR_INVALID_ARG
+    assert call(_fp4(H), _fp4(H), None) == H.HINM_ERR_INVALID_ARG

@@ -3,6 +3,7 @@ activations are in the tails, and every cut of a product, whichever sizes the li
 import numpy as np
 import pytest
 
+import fp4_cuts
 from oracle import fp4_oracle as F
 
 torch = pytest.importorskip("torch")
@@ -141,6 +142,152 @@ def test_gelu_in_both_tails(H, dtype, N, K, transposed, M):
     check_tails(of_bias(H, z, dtype, H.HINM_ACT_GELU, N, K, transposed), gelu64(z64), dtype, own)
     ends = of_bias(H, np.array([np.inf, np.nan], np.float32), dtype, H.HINM_ACT_GELU, N, K, transposed)
     assert ends[0] == np.inf and np.isnan(ends[1])
+
+
+# ----------------------------------------------------------------------------- every cut of a product
+def spread(n, E):
+    """Offsets of E groups in n tokens: the first group empty, the second at most 100, one more empty where
+    there are four, the rest uneven, a few tokens behind the last."""
+    live = n - min(3, n // 8)
+    sizes = np.zeros(E, dtype=np.int64)
+    sizes[1] = min(100, max(1, live // 7))
+    rest = [e for e in range(2, E) if not (e == 3 and E >= 4)]
+    left = live - sizes[1]
+    if not rest:
+        sizes[1] = live
+    for i, e in enumerate(rest):
+        sizes[e] = left - (left // 3) if i + 1 < len(rest) and left > 1 else left
+        left -= sizes[e]
+    return [0] + np.cumsum(sizes).tolist()
+
+
+def whole(seed, rows, K):
+    """0, +-1 .. +-6, which both formats hold whatever the blocks (a 6 in every whole block along either
+    dimension, and in the last column): sums of fewer than 2^24 / 36 products are exact in fp32 in any order."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.tensor([0, 1, 2, 3, 4, 6, -1, -2, -3, -4, -6], device="cuda")
+    x = v[torch.randint(len(v), (rows, K), generator=g, device="cuda")].float()
+    r, c = torch.arange(rows, device="cuda")[:, None], torch.arange(K, device="cuda")[None]
+    x[((r + c) % 16 == 0) | (c == K - 1)] = 6.0
+    return x.bfloat16()
+
+
+class Product:
+    """One product of a kind and its result in 64 bits, from bf16 operands w (of each expert) and x."""
+
+    def __init__(self, H, fmt, kind, M, N, K, E, make):
+        self.H, self.kind, self.M, self.N, self.E = H, kind, M, N, E
+        scale = "amax" if fmt == F.NV else None
+        q = lambda t, **k: H.hinm_fp4_quantize(t, fmt, tensor_scale=scale, **k)  # noqa: E731
+        back = lambda m, **k: H.hinm_fp4_dequantize(m, dtype=torch.float32, **k).double()  # noqa: E731
+        if kind == "plain":
+            self.A, self.B = q(make(1, M, K)), q(make(2, N, K))
+            self.parts = [(slice(0, N), back(self.A), back(self.B))]
+        elif kind == "rows":
+            self.o = spread(N, E)
+            w, x = make(1, E * M, K).view(E, M, K), make(2, N, K)
+            x[self.o[-1]:] = float("nan")
+            self.A = q(w)
+            self.B = q(x, ragged=H.HINM_RAGGED_ROWS, offsets=ints(self.o))
+            a, b = back(self.A), back(self.B)
+            self.parts = [(slice(s, e), a[i], b[s:e]) for i, (s, e) in enumerate(zip(self.o, self.o[1:]))]
+        else:
+            self.o = spread(K, E)
+            d, x = make(1, K, M), make(2, K, N)
+            if make is whole:  # a group's last block may be a part of one
+                last = [e - 1 for e in self.o[1:] if e > 0]
+                d[last], x[last] = 6.0, 6.0
+            d[self.o[-1]:], x[self.o[-1]:] = float("nan"), float("nan")
+            r = dict(axis=0, ragged=H.HINM_RAGGED_DEPTH, offsets=ints(self.o))
+            self.A, self.B = q(d, **r), q(x, **r)
+            a, b = back(self.A, axis=0), back(self.B, axis=0)
+            self.parts = [(i, a[s:e].t(), b[s:e].t()) for i, (s, e) in enumerate(zip(self.o, self.o[1:]))]
+
+    def run(self, dtype, transposed, bias, act, offset, pad):
+        """The outputs of each part as [M][columns], out of a tensor whose other places stay as they were."""
+        H, M, N = self.H, self.M, self.N
+        shape = (self.E, M, N) if self.kind == "depth" else (N, M) if transposed else (M, N)
+        big = torch.full(shape[:-1] + (shape[-1] + offset + pad,), 7.0, dtype=dtype, device="cuda")
+        y = big[..., offset:offset + shape[-1]]
+        if self.kind == "plain":
+            H.hinm_fp4_matmul(self.A, self.B, Y_out=y, transposed=transposed, bias=bias, activation=act)
+        elif self.kind == "rows":
+            H.hinm_fp4_grouped_matmul(self.A, self.B, Y_out=y, transposed=transposed, bias=bias, activation=act)
+        else:
+            H.hinm_fp4_grouped_weight_grad(self.A, self.B, Y_out=y)
+        assert big[..., :offset].eq(7).all() and big[..., offset + shape[-1]:].eq(7).all()
+        if self.kind == "depth":
+            return [y[i] for i, _, _ in self.parts]
+        yt = y.t() if transposed else y
+        if self.kind == "rows":
+            assert yt[:, self.o[-1]:].eq(7).all()
+        return [yt[:, s] for s, _, _ in self.parts]
+
+
+def check_sum(y, a, b, bias, act):
+    """As the products' bound: K + 3 roundings of sum |a b|, the bias's, the activation's slope (at most 1.13)
+    and own error (16 half steps), the store."""
+    h = 2.0 ** -24
+    want, mag = a @ b.t(), a.abs() @ b.abs().t()
+    err = (a.shape[1] + 3) * h * mag
+    if bias is not None:
+        want = want + bias.double()[:, None]
+        err = err + h * (mag + bias.abs().double()[:, None])
+    z = want
+    if act == 2:
+        z = want * torch.sigmoid(want)
+    if act == 3:
+        z = want * 0.5 * torch.special.erfc(-want * 0.5 ** 0.5)
+    if act:
+        err = 1.13 * err + 16 * h * want.abs() + (2.0 ** -16 * z.abs() if y.dtype != torch.float32 else 0)
+    err = err + torch.finfo(y.dtype).eps / 2 * (z.abs() + err)
+    bad = ~((y.double() - z).abs() <= err)
+    assert not bad.any(), (int(bad.sum()), y.double()[bad][:4], z[bad][:4])
+
+
+@FORMATS
+@pytest.mark.parametrize("kind,transposed,columns,pairs,shared,lanes", fp4_cuts.CUTS, ids=str)
+def test_every_cut(H, fmt, kind, transposed, columns, pairs, shared, lanes):
+    sizes = fp4_cuts.find(H, kind, transposed, columns, pairs, shared, lanes)
+    assert sizes, "no size takes this cut on this device"
+    M, N, K, E = sizes
+    c = fp4_cuts.cut(H, kind, M, N, K, E, transposed, fmt)
+    assert (c[0], c[1], c[2] > 1, c[3]) == (columns, pairs, bool(shared), lanes)
+    grad = kind == "depth"
+    # whole numbers: bit for bit, and the same again
+    p = Product(H, fmt, kind, M, N, K, E, whole)
+    first = p.run(torch.float32, transposed, None, 0, 0, 0)
+    for y, (_, a, b) in zip(first, p.parts):
+        assert torch.equal(y.double(), a @ b.t())
+    for y, z in zip(p.run(torch.float32, transposed, None, 0, 0, 0), first):
+        assert torch.equal(y, z)
+    # any numbers; bias and activation; rows of Y that start on 32 bytes, and anywhere
+    p = Product(H, fmt, kind, M, N, K, E, lambda s, *d: rand(s, *d, scale=0.05 if s == 1 else 1.0))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    bias = None if grad else torch.randn((E, M) if kind == "rows" else (M,), generator=g, device="cuda")
+    width = (N if grad or not transposed else M)
+    for dtype, act, offset, pad in ((torch.bfloat16, 3, 0, -width % 16), (torch.float32, 2, 3, 2),
+                                    (torch.float16, 2, 0, 0), (torch.float32, 3, 0, -width % 8),
+                                    (torch.bfloat16, 0, 1, 0)):
+        act = 0 if grad else act
+        for i, (y, (_, a, b)) in enumerate(zip(p.run(dtype, transposed, bias, act, offset, pad), p.parts)):
+            row = bias if bias is None or kind == "plain" else bias[i]
+            check_sum(y, a, b, row, act)
+
+
+@FORMATS
+def test_a_scale_that_is_not_a_number_stays_in_its_row_in_every_cut(H, fmt):
+    for kind, transposed, columns, pairs, shared, lanes in fp4_cuts.CUTS:
+        if kind != "plain":
+            continue
+        M, N, K, _ = fp4_cuts.find(H, kind, transposed, columns, pairs, shared, lanes)
+        w, x = rand(1, M, K), rand(2, N, K)
+        w[M // 2, 5], x[N // 3, K - 1] = float("nan"), float("inf")
+        y = H.hinm_fp4_matmul(H.hinm_fp4_quantize(w, fmt), H.hinm_fp4_quantize(x, fmt), transposed=transposed)
+        y = y.t() if transposed else y
+        nan = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+        nan[M // 2], nan[:, N // 3] = True, True
+        assert torch.equal(y.isnan(), nan)
 
 
 # ----------------------------------------------------------------------------- waits
