@@ -69,6 +69,17 @@ def test_every_call_reports_bad_offsets_by_itself(H, fmt, axis, ragged, o, bad, 
     assert H.hinm_device_status() == want
 
 
+@pytest.mark.parametrize("E,R,C", [(300, 64, 600), (513, 257, 131), (1500, 40, 64), (1200, 128, 300)])
+def test_scales_of_many_matrices(H, E, R, C):
+    """More matrices than the grid has blocks for, each of one block or of several."""
+    x = rand(1, E, R, C) * torch.exp2(torch.arange(E, device="cuda") % 40 - 20)[:, None, None].bfloat16()
+    x[E // 2] = 0
+    q = H.Fp4Matrix.allocate(F.NV, E, R, C, "cuda")
+    got = H.hinm_fp4_tensor_scale(x, q).double().cpu().numpy()
+    amax = x.abs().amax((1, 2)).double().cpu().numpy()
+    assert got.tolist() == [F.pow2_scale([a]) for a in amax]
+
+
 # ----------------------------------------------------------------------------- activations
 def silu64(z):
     e = np.exp(-np.abs(z))
