@@ -207,7 +207,7 @@ __device__ __forceinline__ float silu(float x) {
 }
 // Two at once, in packed instructions: 4096 x 4096 x 512 25.8 us, one by one 30.5.  (Where the columns are
 // held in registers, the pairs' kernel, they cost more than they save: 11008 x 4096 x 4096 105 us, one by
-// one 101, with the quick exponential 95.)
+// one 100, with the quick exponential 95.5.)
 __device__ __forceinline__ void silu2(float& xa, float& xb) {
   using ptx::F2;
   const F2 y(fminf(xa, 128.0f), fminf(xb, 128.0f));
@@ -234,23 +234,27 @@ __device__ __forceinline__ float silu_quick(float x) {
 // from -5.6 on).  An exponential times a polynomial in t is the form of Hastings (Approximations for
 // Digital Computers, 1955); the coefficients are a fit of their own, in relative error over a <= 14.5 (2^-24;
 // 2^-21 as evaluated in fp32).  The exponential is the square of h = 2^(-a^2 log2(e) / 4), which is
-// normal as long as GELU(x) is; its argument's roundings make the error (z^2 + 16) 2^-23 of GELU(z), as
-// large as one half step of z does.  (11008 x 4096 x 4096 bf16 105.5 us, with erff 119, with erfcf 256.)
-__device__ __forceinline__ float gelu(float x) {
-  const float a = fabsf(x);
-  const float t = ptx::rcp(fmaf(a, 0.3f, 1.0f));
-  float w = 0.03840738907456398f;
-  w = fmaf(w, t, -0.16930744051933289f);
-  w = fmaf(w, t, 0.22895173728466034f);
-  w = fmaf(w, t, -0.07683960348367691f);
-  w = fmaf(w, t, 0.14276523888111115f);
-  w = fmaf(w, t, 0.09458588063716888f);
-  w = fmaf(w, t, 0.12194526195526123f);
-  w = fmaf(w, t, 0.11948420852422714f);
-  w = fmaf(w, t, 7.3723608693399e-06f);
-  const float h = ptx::ex2(a * a * -0.36067376022224085f);
-  const float q = (w * h) * h;
-  return x * (x < 0.0f ? q : 1.0f - q);
+// normal as long as GELU(x) is; with its argument's roundings the error is within (z^2 + 16) 2^-23 of
+// GELU(z), in the tail twice what half a step of z makes.  Two at once, in packed instructions: 11008 x 4096 x 4096 bf16 92 us,
+// one by one 107, with erff 120, with erfcf 256.  (One by one, fp32 products of short depth without any
+// activation also took 4 to 6% longer: the registers that the kernel gives this part go short elsewhere.)
+__device__ __forceinline__ void gelu2(float& xa, float& xb) {
+  using ptx::F2;
+  constexpr float kW[9] = {0.03840738907456398f,  -0.16930744051933289f, 0.22895173728466034f,
+                           -0.07683960348367691f, 0.14276523888111115f,  0.09458588063716888f,
+                           0.12194526195526123f,  0.11948420852422714f,  7.3723608693399e-06f};
+  const F2 a(fabsf(xa), fabsf(xb));
+  float u, v;
+  ptx::fma2(a, F2(0.3f, 0.3f), F2(1.0f, 1.0f)).get(u, v);
+  const F2 t(ptx::rcp(u), ptx::rcp(v));
+  F2 w(kW[0], kW[0]);
+#pragma unroll
+  for (int i = 1; i < 9; ++i) w = ptx::fma2(w, t, F2(kW[i], kW[i]));
+  ptx::mul2(ptx::mul2(a, a), F2(-0.36067376022224085f, -0.36067376022224085f)).get(u, v);
+  const F2 h(ptx::ex2(u), ptx::ex2(v));
+  ptx::mul2(ptx::mul2(w, h), h).get(u, v);
+  xa *= xa < 0.0f ? u : 1.0f - u;
+  xb *= xb < 0.0f ? v : 1.0f - v;
 }
 // PRECISE: for outputs in 32 bits.
 template <int ACT, bool PRECISE>
@@ -259,7 +263,10 @@ __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == HINM_ACT_SILU) {
     return PRECISE ? silu(x) : silu_quick(x);
   }
-  if constexpr (ACT == HINM_ACT_GELU) return gelu(x);
+  if constexpr (ACT == HINM_ACT_GELU) {
+    float other = x;
+    gelu2(x, other);
+  }
   return x;
 }
 template <bool PRECISE>
@@ -277,6 +284,9 @@ __device__ __forceinline__ void activate_all(float (&y)[kEpiCols]) {
   if constexpr (ACT == HINM_ACT_SILU && PRECISE && PAIRS) {
 #pragma unroll
     for (int i = 0; i < kEpiCols; i += 2) silu2(y[i], y[i + 1]);
+  } else if constexpr (ACT == HINM_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kEpiCols; i += 2) gelu2(y[i], y[i + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < kEpiCols; ++i) y[i] = activate<ACT, PRECISE>(y[i]);
