@@ -655,6 +655,7 @@ class Fp4Matrix:
                 _fp4_buffer(t, dt, n, name, device)
         c = hinm_fp4(HINM_FP4_LAYOUT_VERSION, self.format, self.batch, self.rows, self.depth,
                      self.ragged, self.groups, at[4], at[1], at[2], at[3])
+        c.aligned = (at[1] | at[2]) % 16 == 0  # values and scales
         object.__setattr__(self, "_c", (at, c))
         return c
 
@@ -779,19 +780,21 @@ def hinm_fp4_quantize(src, format: int, axis: int = 1, bitmask=None, tensor_scal
         if not amax:
             if out.tensor_scale is not tensor_scale:
                 new["tensor_scale"] = tensor_scale
-        elif out._made is None or out.tensor_scale is not out._made or out.given_scale:
-            with _on(stream, dev):
-                new["_made"] = _torch().empty(b, dtype=_torch().float32, device=src.device)
-            new["tensor_scale"] = new["_made"]
-        if out.given_scale == amax:
-            new["given_scale"] = not amax
+            if not out.given_scale:
+                new["given_scale"] = True
+        else:
+            g = out.tensor_scale
+            if g is None or g is not out._made or out.given_scale:
+                with _on(stream, dev):
+                    g = _torch().empty(b, dtype=_torch().float32, device=src.device)
+                new.update(tensor_scale=g, _made=g, given_scale=False)
     # what changes goes into a copy of the description, which `out` takes over once the call has been
     # accepted: a refused call, whichever side refuses it, leaves `out` as it was
     q = out._changed(new) if new else out
     as_c = q.as_c(dev)
     cq, p, m = ctypes.byref(as_c), src.data_ptr(), _ptr(bitmask)
     if amax:
-        if ((as_c.values or 0) | (as_c.scales or 0)) & 15:  # (the scale's own call does not look at them)
+        if not as_c.aligned:  # (the scale's own call does not look at the other buffers)
             raise ValueError("Fp4Matrix: need values and scales on 16-byte boundaries")
         _check(_lib.hinm_fp4_tensor_scale(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_tensor_scale")
     _check(_lib.hinm_fp4_quantize(p, code, ld, bs, axis, m, cq, s), "hinm_fp4_quantize")
