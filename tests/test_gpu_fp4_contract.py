@@ -301,6 +301,61 @@ def test_a_scale_that_is_not_a_number_stays_in_its_row_in_every_cut(H, fmt):
         assert torch.equal(y.isnan(), nan)
 
 
+@FORMATS
+def test_products_of_pairs_at_once_and_replayed(H, fmt):
+    """The pairs' kernel, which takes the whole GPU, on two streams at once, and out of a graph whose operands
+    change under it."""
+    sizes = [fp4_cuts.find(H, kind, False, 256, 1, 0, False) for kind in ("plain", "rows", "depth")]
+    products = [Product(H, fmt, kind, *size, whole) for kind, size in zip(("plain", "rows", "depth"), sizes)]
+    want = [[a @ b.t() for _, a, b in p.parts] for p in products]
+    streams = [torch.cuda.Stream() for _ in products]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, s in zip(products, streams):
+            with torch.cuda.stream(s):
+                got.append((p, p.run(torch.float32, False, None, 0, 0, 0)))
+    torch.cuda.synchronize()
+    for p, ys in got:
+        for y, z in zip(ys, want[products.index(p)]):
+            assert torch.equal(y.double(), z)
+    M, N, K, _ = sizes[0]
+    x, w = whole(5, N, K), products[0].A
+    q = H.hinm_fp4_quantize(x, fmt)
+    Y = torch.empty(M, N, device="cuda")
+    H.hinm_fp4_quantize(x, fmt, out=q)
+    H.hinm_fp4_matmul(w, q, Y_out=Y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        H.hinm_fp4_quantize(x, fmt, out=q)
+        H.hinm_fp4_matmul(w, q, Y_out=Y)
+    for seed in (6, 7):
+        x.copy_(whole(seed, N, K))
+        Y.zero_()
+        g.replay()
+        assert torch.equal(Y.double(), products[0].parts[0][1] @ x.double().t())
+    del g
+
+
+@FORMATS
+@pytest.mark.parametrize("axis", [1, 0])
+def test_batches_of_a_larger_tensor(H, fmt, axis):
+    """Matrices and rows a stride apart, on the way in and back."""
+    big = torch.full((7, 90, 150), float("nan"), dtype=torch.bfloat16, device="cuda")
+    view = big[1::2, 5:85:2, 8:136]        # every other matrix and row
+    view.copy_(rand(3, 3, 40, 128))
+    scale = "amax" if fmt == F.NV else None
+    a = H.hinm_fp4_quantize(view, fmt, axis=axis, tensor_scale=scale)
+    b = H.hinm_fp4_quantize(view.contiguous(), fmt, axis=axis, tensor_scale=scale)
+    want = H.hinm_fp4_dequantize(b, axis=axis)
+    out = torch.full_like(big, 5.0)
+    H.hinm_fp4_dequantize(a, axis=axis, out=out[1::2, 5:85:2, 8:136])
+    assert torch.equal(out[1::2, 5:85:2, 8:136], want)
+    out[1::2, 5:85:2, 8:136] = 5.0
+    assert out.eq(5).all()
+
+
 # ----------------------------------------------------------------------------- waits
 def test_a_product_that_lasts_longer_than_a_wait_may(H):
     """Waits inside the kernels are limited to 2 s each.  A product of 1.9e16 operations takes longer than that
