@@ -21,11 +21,12 @@
 //   2..9   epilogue: 32 lanes of the accumulator and half of its columns each, 32 or 64 columns
 //          at a time, through a tile in shared memory, so that Y is written in whole 128-byte
 //          lines
-// What bounds it, measured at 4096 x 4096 x 16384 (pairs): NV takes 115.6 us, 109 without the
-// copies of the scales, 109 without the loads, 90 without both; MX 104.0, 103.7, 90.7, 83.5.  A
-// stage of 256 x 256 x 256 is 542 cycles of products at the nominal rate and takes 830 (NV) and
-// 740 (MX): the instructions that issue it, the 12 (6) scale copies among them, and 39 (36) KB a
-// stage into each SM's shared memory bind together.
+// What bounds it, measured at 4096 x 4096 x 16384 (pairs): NV takes 115.6 us, MX 104.0, and copies of
+// this kernel with parts left out 109 and 103.7 (no copies of scales), 109 and 90.7 (no loads), 90 and
+// 83.5 (neither).  A stage of 256 x 256 x 256 is 542 cycles of products at the nominal rate and takes
+// 830 (NV) and 740 (MX): the instructions that issue it, the 12 (6) scale copies among them, and 39 (36)
+// KB a stage into each SM's shared memory bind together.  At 11008 x 4096 x 4096 with SiLU the tensor
+// cores are busy for 44% of the time: a pair has one accumulator, and between two tiles it changes hands.
 // The scales of a stage wait in a slot of tensor-memory columns, which is written again only
 // after the products that read it are done (the commit that frees their stage).  With few
 // tiles a cluster shares one tile's depth (SPLIT): each CTA leaves its partial sums in its own
@@ -491,8 +492,8 @@ __device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool 
   }
 }
 
-// Any columns and rows: read as they are worked on (beside write_lines' held columns, holding these
-// too made the kernel of pairs spill).
+// Any columns and rows: read as they are worked on.  (The kernel of pairs, with write_lines' held columns,
+// already keeps 132 bytes of a thread, in the activations, outside of its 168 registers.)
 template <int DT, int COLS, bool BIASQ, class Done>
 __device__ __forceinline__ void write_any(const MmArgs& a, uint32_t acc, bool zero,
                                           const Columns& c, Done done) {
@@ -1066,6 +1067,11 @@ struct Plan {
 // Sharing a tile's depth costs 1.5 us and 0.03 a column (partial sums through the cluster): 4096
 // rows of depth 4096 by 1 column 7.1 us shared by four and 9.5 not, by 256 columns 13.1 shared by
 // two and 10.4 not.
+// A stage costs the same whatever the number of columns that are real, and few tokens over much depth
+// take 128 columns (from 11008 x 8192 on) or pairs (32000 x 32768): right for 32 and 64 tokens (11008 x
+// 8192 MX 14.9 and 14.7 us, in 64 columns 17.4 and 19.8) and about even for 16, but a single token loses
+// where tiles go round several times (32000 x 8192 NV 39.7 us, in 64 columns 30.7; at 11008 x 8192 15.7
+// and 16.2).
 // p, q: rows of P and Q, in `groups` ragged parts when given (tokens: p_ragged or not).
 Plan make_plan(long long p, long long q, long long depth, int p_groups, int q_groups, int times,
                int sms) {

@@ -12,8 +12,11 @@
 // an fp32 number, x' differs from it by at least one unit in its last place, and the quotient
 // from the border by more than half a unit (by a whole representable step below 0.25).
 //
-// The kernels are bound by DRAM: a bf16 element costs 2 bytes in and 0.5 + 1/16 (NV) or
-// 0.5 + 1/32 (MX) bytes out.
+// A bf16 element costs 2 bytes in and 0.5 + 1/16 (NV) or 0.5 + 1/32 (MX) bytes out; at 11008 x 4096
+// the kernels take 1.2 to 1.5 times as long as these bytes at the rate of a copy (NV along the rows
+// 23.4 us for 17.6 of bytes, with a mask 27.7 for 18.5, down the columns 26.7; MX 21.4 and 21.9 for
+// 17.4).  What holds them besides DRAM is the arithmetic of an element: with a mask along the rows the
+// issue slots are 59% taken (DRAM 39%), down the columns registers leave a quarter of the warps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -621,11 +624,12 @@ __device__ __forceinline__ uint4 piece_of(const Around& r) {
 // sector.  A block of 32 lies in two neighbouring lanes.  (Two columns and 64 of the depth a thread,
 // with 4-byte loads, took 22.6 us at 4096 x 4096 bf16 NV and 33.6 us MX; this takes 11.2 and 8.9.)
 // ALIGNED: rows are aligned and of whole pieces.
-// Blocks an SM, which bound a thread's registers: 16-bit elements five (11008 x 4096 bf16 NV 27.2 us,
-// with a mask 32.6; as many registers as are wanted, four and three blocks, 28.5 and 37.7; six would
-// spill), rows that start anywhere four (3598 x 10954 bf16 NV 34.1 us and 44.6, with five 36.9 and
-// 60.1); fp32 six (8192 x 8192 NV 50 us, else 58), but with a mask's 16 bytes beside the elements
-// five (11008 x 4096 NV 44.0 us, with six 73.8).
+// Blocks an SM, which bound a thread's registers: 16-bit elements five (11008 x 4096 bf16 NV 26.7 us,
+// with a mask 32.0, although both keep 16 to 32 bytes of a thread outside of its 96 registers; with four
+// and three blocks, as many registers as are wanted, 28.5 and 37.7), rows that start anywhere four
+// (3598 x 10954 bf16 NV 33.7 us and, spilling 40 bytes, 44.6; with five 36.9 and 60.1); fp32 six (8192 x
+// 8192 NV 50 us, else 58), but with a mask's 16 bytes beside the elements five (11008 x 4096 NV 43.5 us,
+// with six 73.8).
 template <int DT, int FMT, bool MASK, bool ALIGNED>
 __global__ void __launch_bounds__(kQThreads, DT == HINM_DTYPE_F32 ? (MASK ? 5 : 6) : ALIGNED ? 5 : 4)
     quant_pieces_kernel(const QArgs a) {
@@ -903,8 +907,8 @@ __global__ void __launch_bounds__(kQWarps * 32) dequant_rows_kernel(const QArgs 
 }
 
 // The way back for what quant_pieces_kernel takes: the same share of a thread.
-// (Five blocks an SM for MX: 8192 x 8192 bf16 37.6 us instead of 39.6; NV, whose table takes
-// registers, 46.9 instead of 37.5.)
+// (Five blocks an SM for MX, with 44 bytes of a thread outside of its registers: 8192 x 8192 bf16 37.6 us
+// instead of 39.6; NV, which would keep more there, 46.9 instead of 37.5.)
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kQThreads, FMT == HINM_FP4_MX ? 5 : 1) dequant_pieces_kernel(const QArgs a) {
   ptx::enter_dependent();
