@@ -440,9 +440,9 @@ hinm_status hinm_spmm_epilogue(const hinm_layout* layout, const void* X, int N, 
  * of the token dimension, which has `rows` (HINM_RAGGED_ROWS) or `depth` (HINM_RAGGED_DEPTH)
  * places in all; tokens before the first or behind the last group count for nothing and their
  * places are not written.  offsets: device int32 [groups + 1], nondecreasing, inside the
- * dimension; every call that is given others sets HINM_ERR_INVALID_ARG in the device status
- * word, reads and writes nothing outside the matrices, and leaves what it writes unspecified
- * (the products write nothing).
+ * dimension; every call that works on a matrix (of some rows and depth) with others sets
+ * HINM_ERR_INVALID_ARG in the device status word, reads and writes nothing outside the matrices,
+ * and leaves what it writes unspecified (the products write nothing).
  *   ragged rows:  values as above; group e's scale tiles start at tile offsets[e] / 128 + e
  *                 (rows / 128 + groups tiles, division rounded down)
  *   ragged depth: D = 128 (depth / 128 + groups); group e's tokens start at stored depth

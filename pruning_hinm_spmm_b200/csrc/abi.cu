@@ -1041,7 +1041,7 @@ hinm_status hinm_selftest_fp4_cut(const hinm_fp4* A, const hinm_fp4* B, int tran
   const bool by_depth = B->ragged == HINM_RAGGED_DEPTH;
   if (A->ragged != (by_depth ? HINM_RAGGED_DEPTH : HINM_RAGGED_NONE) ||
       (by_depth ? A->groups != B->groups
-                : A->batch != (B->ragged == HINM_RAGGED_ROWS ? B->groups : B->batch)))
+                : A->batch != (B->ragged == HINM_RAGGED_ROWS ? B->groups : 1) || B->batch != 1))
     return fail(HINM_ERR_UNSUPPORTED, "no product takes these matrices together");
   hinm::Fp4Cut c{};
   if (B->rows > 0) c = hinm::fp4_cut(*A, *B, transposed != 0);

@@ -278,3 +278,4 @@ def test_cut_of_a_product(H):
     assert call(_fp4(H, batch=3), _fp4(H, ragged=1, groups=2)) == H.HINM_ERR_UNSUPPORTED
     assert L.hinm_selftest_fp4_cut(None, None, 0, out) == H.HINM_ERR_INVALID_ARG
     assert call(_fp4(H), _fp4(H), None) == H.HINM_ERR_INVALID_ARG
+    assert call(_fp4(H, batch=2), _fp4(H, batch=2)) == H.HINM_ERR_UNSUPPORTED
