@@ -233,12 +233,13 @@ __device__ __forceinline__ float silu_quick(float x) {
 // GELU(x) = x Phi(x), Phi(-a) = erfc(a / sqrt 2) / 2 = e^(-a^2/2) w(t), t = 1 / (1 + 0.3 a): without a
 // difference of nearly equal numbers for either sign (1 + erf(x / sqrt 2) has none of its digits right
 // from -5.6 on).  An exponential times a polynomial in t is the form of Hastings (Approximations for
-// Digital Computers, 1955); the coefficients are a fit of their own, in relative error over a <= 14.5 (2^-24;
-// 2^-21 as evaluated in fp32).  The exponential is the square of h = 2^(-a^2 log2(e) / 4), which is
-// normal as long as GELU(x) is; with its argument's roundings the error is within (z^2 + 16) 2^-23 of
-// GELU(z), in the tail twice what half a step of z makes.  Two at once, in packed instructions: 11008 x 4096 x 4096 bf16 92 us,
-// one by one 107, with erff 120, with erfcf 256.  (One by one, fp32 products of short depth without any
-// activation also took 4 to 6% longer: the registers that the kernel gives this part go short elsewhere.)
+// Digital Computers, 1955); the coefficients are a fit of their own, in relative error over a <= 14.5
+// (2^-24; 2^-21 as evaluated in fp32).  The exponential is the square of h = 2^(-a^2 log2(e) / 4), which
+// is normal as long as GELU(x) is; with its argument's roundings the error is within (z^2 + 16) 2^-23 of
+// GELU(z), in the tail twice what half a step of z makes.  Two at once, in packed instructions: 11008 x
+// 4096 x 4096 bf16 92 us, one by one 107, with erff 120, with erfcf 256.  (One by one, fp32 products of
+// short depth without any activation also took 4 to 6% longer: the registers that the kernel gives this
+// part go short elsewhere.)
 __device__ __forceinline__ void gelu2(float& xa, float& xb) {
   using ptx::F2;
   constexpr float kW[9] = {0.03840738907456398f,  -0.16930744051933289f, 0.22895173728466034f,
@@ -1110,7 +1111,7 @@ struct Choice {
 };
 Choice choose(const hinm_fp4& A, const hinm_fp4& B, bool transposed) {
   const bool by_rows = B.ragged == HINM_RAGGED_ROWS, by_depth = B.ragged == HINM_RAGGED_DEPTH;
-  const int n = by_rows ? (B.rows + B.groups - 1) / B.groups : B.rows;
+  const long long n = by_rows ? ((long long)B.rows + B.groups - 1) / B.groups : B.rows;
   Choice c;
   c.swap = transposed && n > 64;
   const int groups = by_rows ? B.groups : 0;

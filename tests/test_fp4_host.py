@@ -279,3 +279,6 @@ def test_cut_of_a_product(H):
     assert L.hinm_selftest_fp4_cut(None, None, 0, out) == H.HINM_ERR_INVALID_ARG
     assert call(_fp4(H), _fp4(H), None) == H.HINM_ERR_INVALID_ARG
     assert call(_fp4(H, batch=2), _fp4(H, batch=2)) == H.HINM_ERR_UNSUPPORTED
+    # as many tokens as there may be: their number and the groups' do not overflow
+    assert cut("rows", 64, 0x7FFFFF00, 1, 512, True)[3] == 1
+    assert cut("rows", 64, 0x7FFFFF00, 1, 512, False)[3] == 0
