@@ -417,7 +417,7 @@ struct Columns {
 };
 
 // PC columns (64 or 128 bytes of Y), from column `col` on, into the staging tile.
-template <int DT, int PC, bool BIASQ, bool LINES, bool HELD>
+template <int DT, int PC, bool BIASQ, bool LINES, bool HELD, bool ACTS>
 __device__ __forceinline__ void stage_columns(const MmArgs& a, const Columns& c, int col,
                                               const uint32_t* v) {
   constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
@@ -431,7 +431,7 @@ __device__ __forceinline__ void stage_columns(const MmArgs& a, const Columns& c,
                   BIASQ ? __ldg(c.bias_cols + (LINES ? col + h + i : min(col + h + i, c.cols - 1)))
                         : c.bias_row);
     constexpr bool kPrecise = DT == HINM_DTYPE_F32;
-    if (a.act == HINM_ACT_NONE) {
+    if (!ACTS || a.act == HINM_ACT_NONE) {
     } else if (a.act == HINM_ACT_RELU) activate_all<HINM_ACT_RELU, kPrecise>(f);
     else if (a.act == HINM_ACT_SILU) activate_all<HINM_ACT_SILU, kPrecise, !HELD>(f);
     else if (a.act == HINM_ACT_GELU) activate_all<HINM_ACT_GELU, kPrecise>(f);
@@ -452,7 +452,7 @@ __device__ __forceinline__ void stage_columns(const MmArgs& a, const Columns& c,
 // read first, and `done` is called, so that the accumulator is free while they are worked on (pairs
 // at 11008 x 4096 x 4096: 86.8 us, else 89.5; with two accumulators it costs registers for nothing:
 // 4096 x 4096 x 1024 in 128 x 192 tiles 18.4 us, else 17.1).
-template <int DT, int COLS, bool BIASQ, bool HOLD, class Done>
+template <int DT, int COLS, bool BIASQ, bool HOLD, bool ACTS, class Done>
 __device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool zero,
                                             const Columns& c, Done done) {
   constexpr int es = DT == HINM_DTYPE_F32 ? 4 : 2;
@@ -475,7 +475,7 @@ __device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool 
       read_columns<PC>(acc + col, zero, v);
       if (col + PC >= COLS) done();
     }
-    stage_columns<DT, PC, BIASQ, true, HOLD>(a, c, col, HOLD ? v + col : v);
+    stage_columns<DT, PC, BIASQ, true, HOLD, ACTS>(a, c, col, HOLD ? v + col : v);
     __syncwarp();
     char* yo = yr + col * es;
 #pragma unroll
@@ -493,9 +493,9 @@ __device__ __forceinline__ void write_lines(const MmArgs& a, uint32_t acc, bool 
   }
 }
 
-// Any columns and rows: read as they are worked on.  (The kernel of pairs, with write_lines' held columns,
-// already keeps 132 bytes of a thread, in the activations, outside of its 168 registers.)
-template <int DT, int COLS, bool BIASQ, class Done>
+// Any columns and rows: read as they are worked on.  (The kernels of pairs, with write_lines' held columns,
+// already keep 116 bytes of a thread, and 132 with the activations, outside of their 168 registers.)
+template <int DT, int COLS, bool BIASQ, bool ACTS, class Done>
 __device__ __forceinline__ void write_any(const MmArgs& a, uint32_t acc, bool zero,
                                           const Columns& c, Done done) {
   constexpr int PC = DT != HINM_DTYPE_F32 && COLS % 64 == 0 ? 64 : 32;
@@ -504,7 +504,7 @@ __device__ __forceinline__ void write_any(const MmArgs& a, uint32_t acc, bool ze
     uint32_t v[PC];
     read_columns<PC>(acc + col, zero, v);
     if (col + PC >= c.cols) done();
-    stage_columns<DT, PC, BIASQ, false, false>(a, c, col, v);
+    stage_columns<DT, PC, BIASQ, false, false, ACTS>(a, c, col, v);
     __syncwarp();
     write_tile(a, c.tile, c.lane, c.rows, min(PC, c.cols - col), c.at0 + col);
     __syncwarp();
@@ -531,7 +531,10 @@ __device__ __forceinline__ void store_four(const MmArgs& a, const float (&y)[4],
   }
 }
 
-template <int FMT, int BN, bool SPLIT, bool PAIR>
+// ACTS: with the activations' code.  The two larger tiles have a kernel without it for products that take
+// none, since what it asks for in registers costs the rest: 16 experts' weight gradients of 2048 x 1024,
+// 8111 tokens, 38.5 us, with it 40.6; a prompt's 16 products of 4096 x 2048 77.0 and 78.2.
+template <int FMT, int BN, bool SPLIT, bool PAIR, bool ACTS>
 __global__ void __launch_bounds__(kMmThreads, 1)
     fp4_mm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmSp, const __grid_constant__ CUtensorMap tmSq,
@@ -855,11 +858,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           auto write = [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
             if (cw.bias_cols) {
-              if (lines) write_lines<DT, kOwn, true, C::kAccBufs == 1>(a, lanes + col0, s1 == s0, cw, done);
-              else write_any<DT, kOwn, true>(a, lanes + col0, s1 == s0, cw, done);
+              if (lines) write_lines<DT, kOwn, true, C::kAccBufs == 1, ACTS>(a, lanes + col0, s1 == s0, cw, done);
+              else write_any<DT, kOwn, true, ACTS>(a, lanes + col0, s1 == s0, cw, done);
             } else {
-              if (lines) write_lines<DT, kOwn, false, C::kAccBufs == 1>(a, lanes + col0, s1 == s0, cw, done);
-              else write_any<DT, kOwn, false>(a, lanes + col0, s1 == s0, cw, done);
+              if (lines) write_lines<DT, kOwn, false, C::kAccBufs == 1, ACTS>(a, lanes + col0, s1 == s0, cw, done);
+              else write_any<DT, kOwn, false, ACTS>(a, lanes + col0, s1 == s0, cw, done);
             }
           };
           if (a.dtype == HINM_DTYPE_BF16) write(std::integral_constant<int, HINM_DTYPE_BF16>{});
@@ -1031,10 +1034,10 @@ struct Maps {
   CUtensorMap p, q, sp, sq;  // values; scales (pairs)
 };
 
-template <int FMT, int BN, bool SPLIT, bool PAIR>
+template <int FMT, int BN, bool SPLIT, bool PAIR, bool ACTS>
 cudaError_t run(MmArgs a, const Maps& m, long long tiles, cudaStream_t s) {
   using C = MmCfg<FMT, BN, PAIR>;
-  auto kernel = fp4_mm_kernel<FMT, BN, SPLIT, PAIR>;
+  auto kernel = fp4_mm_kernel<FMT, BN, SPLIT, PAIR, ACTS>;
   cudaError_t e = set_max_dynamic_smem((const void*)kernel, (int)C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if constexpr (!SPLIT && !PAIR) {
@@ -1134,9 +1137,12 @@ cudaError_t launch_tiles(MmArgs a, const Maps& m, const Plan& p, cudaStream_t s)
   if (tiles > 0x3FFFFFFFll) return cudaErrorInvalidValue;
   a.split = p.split;
   if constexpr (BN <= 128 && !PAIR) {
-    if (p.split > 1) return run<FMT, BN, true, false>(a, m, tiles, s);
+    if (p.split > 1) return run<FMT, BN, true, false, true>(a, m, tiles, s);
   }
-  return run<FMT, BN, false, PAIR>(a, m, tiles, s);
+  if constexpr (BN > 128) {
+    if (a.act == HINM_ACT_NONE) return run<FMT, BN, false, PAIR, false>(a, m, tiles, s);
+  }
+  return run<FMT, BN, false, PAIR, true>(a, m, tiles, s);
 }
 
 template <int FMT>
